@@ -343,6 +343,133 @@ int flashspmm_predict_us(int32_t M, int32_t K, int32_t N, int64_t nnz, int32_t n
                          double* t_dense);
 int flashspmm_prefer_sparse(int32_t M, int32_t K, int32_t N, int64_t nnz, int32_t num_sms);
 
+/* ---------------------------------------------------------------- 4-bit weights
+ *
+ * The other compressed form of a weight for the same skinny products: 4-bit
+ * codes q in 0..15 with one 16-bit scale s (and one zero point z) for each
+ * group of neighbours along K,
+ *
+ *   w = s * (q - z),   z = 8 where no zero points are kept.
+ *
+ * It holds every entry of A, so it serves weights that are not pruned. */
+
+/* Element types of the calls below. */
+enum { FLASHSPMM_F16 = 0, FLASHSPMM_BF16 = 1, FLASHSPMM_F32 = 2 };
+
+/* Activations of flashspmm_moe_w4: v / (1 + exp(-v)), v * Phi(v) (with erf), max(v, 0). */
+enum { FLASHSPMM_ACT_SILU = 0, FLASHSPMM_ACT_GELU = 1, FLASHSPMM_ACT_RELU = 2 };
+
+/* A view of `count` 4-bit matrices of M x K one behind the other (1: a single
+ * weight).  The buffers are the caller's, of flashspmm_w4_sizes bytes, written
+ * by flashspmm_w4_encode or flashspmm_w4_pack.
+ *
+ * Layout: strips of 16 rows times units of 128 columns, both padded with zero
+ * weights; unit (matrix, strip, u) takes 1024 bytes of codes at
+ * ((matrix * ceil(M/16) + strip) * ceil(K/128) + u) * 1024, ordered so that
+ * lane 4 g + t of a warp finds the codes of its tensor-core fragments (rows g
+ * and g + 8, columns 32 b + 8 t .. + 7 of each 32-column block b) in two
+ * 16-byte loads.  Scales and zero points of a unit are
+ * [8][128 / group][2] entries: [g][group][row g, row g + 8]. */
+typedef struct {
+  int32_t M, K;          /* rows and columns of one matrix, each <= 2^30 */
+  int32_t count;         /* matrices, >= 1 */
+  int32_t group;         /* columns that share a scale: 32, 64 or 128 */
+  int32_t dtype;         /* FLASHSPMM_F16 or FLASHSPMM_BF16: of the scales and of the activations they meet */
+  int32_t reserved;      /* must be 0 */
+  void* codes;           /* device, 16-byte aligned */
+  void* scales;          /* device, `dtype`, 16-byte aligned */
+  uint8_t* zeros;        /* device, 16-byte aligned; NULL: every zero point is 8 */
+} flashspmm_w4;
+
+/* Bytes of codes and entries of scales and of zero points that a view of these
+ * sizes holds.  Any output may be NULL.  0, or -1 on bad arguments. */
+int flashspmm_w4_sizes(int32_t M, int32_t K, int32_t count, int32_t group, int64_t* codes_bytes, int64_t* scales,
+                       int64_t* zeros);
+
+/* Encoder: a dense weight to A's buffers.
+ *   W          device, A->dtype, count * M rows of K values, ldw values apart.
+ *   symmetric  1: s = max|w| / 7, z = 8 (A->zeros must be NULL).
+ *              0: s = (max(w, 0) - min(w, 0)) / 15, z = round(-min(w, 0) / s)
+ *              clamped to 0..15 (A->zeros must be there).
+ * s is rounded to A->dtype and q = clamp(round(w / s) + z, 0, 15); roundings
+ * are to nearest, ties to even.  A group whose s is zero has q = z.  A group
+ * with a NaN or an infinity gets such a scale, so it decodes to values that
+ * are not finite. */
+flashspmm_status flashspmm_w4_encode(const void* W, int64_t ldw, int32_t symmetric, const flashspmm_w4* A,
+                                     void* stream);
+
+/* Lays out codes that the caller has (a checkpoint quantised elsewhere).
+ *   codes   device uint8[count * M][K], one code each, the low 4 bits are used.
+ *   scales  device, A->dtype, [count * M][ceil(K / group)].
+ *   zeros   device uint8 of the same shape, 0..127 (the low 7 bits are used);
+ *           NULL if and only if A->zeros is NULL. */
+flashspmm_status flashspmm_w4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                                   const flashspmm_w4* A, void* stream);
+
+/* Decoder: W[count * M][K] = s * (q - z), rounded once to w_dtype (A->dtype or
+ * FLASHSPMM_F32, where it is exact unless it overflows). */
+flashspmm_status flashspmm_w4_decode(const flashspmm_w4* A, void* W, int32_t w_dtype, void* stream);
+
+/* Bytes of workspace that flashspmm_w4_matmul needs for these arguments on the
+ * current device; 0 when none. */
+size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B, int64_t ldb, int32_t N);
+
+/* Skinny product C = A x B with fp32 sums.
+ *   A          a view with count = 1.
+ *   B          device, A->dtype, N rows of K activations, ldb values apart
+ *              (any alignment; rows that start on 16 bytes with K % 8 == 0 are
+ *              read as they are, others are copied to the workspace first).
+ *   C          device, c_dtype = A->dtype or FLASHSPMM_F32, N rows of M values,
+ *              ldc values apart.  Nothing between the rows is written.
+ *   N          1 .. 256.
+ *   workspace  device, 16-byte aligned, flashspmm_w4_matmul_workspace_bytes;
+ *              needs no initialisation.  Calls that may run concurrently need
+ *              separate ones.
+ * Results are deterministic.  K == 0 writes zeros; M == 0 or N == 0 does
+ * nothing. */
+flashspmm_status flashspmm_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc,
+                                     int32_t c_dtype, int32_t N, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Bytes of workspace that flashspmm_moe_w4 needs for these arguments. */
+size_t flashspmm_moe_w4_workspace_bytes(const flashspmm_w4* gate, const void* X, int64_t ldx, int32_t tokens,
+                                        int32_t top_k);
+
+/* A mixture-of-experts layer for a few tokens:
+ *
+ *   logits = router x
+ *   ids    = the top_k largest logits, largest first, ties to the lower index
+ *   p      = softmax over the chosen logits (renormalize = 1) or, at the
+ *            chosen ones, over all (0)
+ *   h_e    = act(gate_e x) * (up_e x), or act(gate_e x) with up = NULL
+ *   out    = sum over the chosen experts of p * (down_e h_e)
+ *
+ *   gate, up   views of E matrices F x H; down: E matrices H x F.  The same
+ *              group and dtype in all; zero points may differ.
+ *   X          device, dtype, `tokens` rows of H, ldx values apart (alignment
+ *              as in flashspmm_w4_matmul).
+ *   router     device, E x H row-major, dtype or FLASHSPMM_F32 (router_dtype).
+ *              Logits are summed in 64 bits, so the choice does not depend on
+ *              the order of a sum.  A NaN logit is chosen last and its token's
+ *              p are NaN.
+ *              NULL: ids and weights are inputs, a routing of the caller's.
+ *              An id outside 0 .. E - 1 contributes nothing, one named twice
+ *              by a token counts with the sum of its weights.
+ *   ids        device int32[tokens][top_k];  weights  device float[tokens][top_k]:
+ *              outputs with a router, inputs without.
+ *   out        device, dtype, `tokens` rows of H, ldo values apart.  A token
+ *              that no expert takes gets zeros.
+ *   tokens     0 .. 64;  E <= 512;  top_k 1 .. 16 (<= E with a router).
+ *   workspace  device, 16-byte aligned; needs no initialisation.  Calls that
+ *              may run concurrently need separate ones.
+ * Products are summed in fp32 and h is rounded to dtype between them (with fp16
+ * an h beyond 65504 becomes infinite, as in a layer of separate fp16 calls).
+ * Results are deterministic. */
+flashspmm_status flashspmm_moe_w4(const flashspmm_w4* gate, const flashspmm_w4* up, const flashspmm_w4* down,
+                                  const void* X, int64_t ldx, const void* router, int32_t router_dtype, int32_t tokens,
+                                  int32_t top_k, int32_t renormalize, int32_t activation, int32_t* ids, float* weights,
+                                  void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the library's device status
  * word for the current device: FLASHSPMM_OK or the first error a kernel
  * recorded since the last read. */

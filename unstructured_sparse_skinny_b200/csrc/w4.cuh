@@ -1,0 +1,344 @@
+// 4-bit weights with group scales: layout, launchers and the warp-level
+// product shared by the skinny matrix product and the experts' products.
+//
+// Layout.  A matrix of M x K codes is cut into strips of 16 rows and units of
+// 128 columns; unit (strip, u) is 1024 bytes at (strip * units + u) * 1024.
+// A warp reads it with two 16-byte loads per lane, and every lane then holds
+// exactly the codes of its own mma.m16n8k16 A fragments, so nothing is
+// shuffled or staged.  Lane l = 4 * g + t owns rows g and g + 8 and, in each
+// 32-column block b of the unit, the eight columns 32 * b + 8 * t .. + 7.  The
+// order of K inside a product is free as long as both operands use the same
+// one: step s of block b takes columns 8 * t + 4 * s + {0, 1} as the
+// fragment's first column pair and + {2, 3} as its second, so the B fragments
+// of a block are one 16-byte load of eight neighbouring activations.  A block
+// is 32 columns of K in every lane, so groups of 32, 64 and 128 columns end on
+// block boundaries.  Word (b, s) of a lane is the (2 * (b & 1) + s)-th of its
+// 16-byte load b / 2; its nibble i holds the first and nibble i + 4 the second
+// value of fragment register a_i (a0: row g, first pair; a1: row g + 8, first;
+// a2: row g, second; a3: row g + 8, second).
+//
+// Scales (16 bits) and zero points (8 bits) of a unit are [g][group][row g,
+// row g + 8], so a lane reads all it needs of a unit in one load.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace flashspmm {
+
+constexpr int kW4StripRows = 16;
+constexpr int kW4UnitCols = 128;
+constexpr int kW4UnitBytes = 1024;
+
+// A stack of 4-bit matrices as the kernels see it.
+struct W4Dev {
+  const uint4* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;  // nullptr: every zero point is 8
+  int32_t M, K;
+  int32_t strips;  // of one matrix
+  int32_t units;   // of one strip
+  int32_t group;
+};
+
+__host__ __device__ inline int32_t w4_strips(int32_t M) {
+  return static_cast<int32_t>((static_cast<int64_t>(M) + kW4StripRows - 1) / kW4StripRows);
+}
+__host__ __device__ inline int32_t w4_units(int32_t K) {
+  return static_cast<int32_t>((static_cast<int64_t>(K) + kW4UnitCols - 1) / kW4UnitCols);
+}
+
+inline W4Dev w4_dev(const flashspmm_w4* A) {
+  W4Dev d;
+  d.codes = static_cast<const uint4*>(A->codes);
+  d.scales = static_cast<const uint16_t*>(A->scales);
+  d.zeros = A->zeros;
+  d.M = A->M;
+  d.K = A->K;
+  d.strips = w4_strips(A->M);
+  d.units = w4_units(A->K);
+  d.group = A->group;
+  return d;
+}
+
+// ---------------------------------------------------------------- 16-bit types
+
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T>
+__device__ __forceinline__ float bits_to_float(uint16_t b);
+template <>
+__device__ __forceinline__ float bits_to_float<__half>(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+template <>
+__device__ __forceinline__ float bits_to_float<__nv_bfloat16>(uint16_t b) {
+  return __uint_as_float(static_cast<uint32_t>(b) << 16);
+}
+
+// ---------------------------------------------------------------- codes to A fragments
+
+// (a & b) | c in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// The pair {z, z} (first row) and its like for the second row, in the form
+// that w4_fragment subtracts.
+template <typename T>
+struct W4Zero;
+template <>
+struct W4Zero<__half> {
+  __half2 lo, hi;  // 1024 + z, -(64 + z')
+  __device__ __forceinline__ W4Zero(int z0, int z1)
+      : lo(__half2half2(__int2half_rn(1024 + z0))), hi(__half2half2(__int2half_rn(-64 - z1))) {}
+};
+template <>
+struct W4Zero<__nv_bfloat16> {
+  __nv_bfloat162 lo, hi;  // 128 + z, 128 + z'
+  __device__ __forceinline__ W4Zero(int z0, int z1)
+      : lo(__bfloat162bfloat162(__int2bfloat16_rn(128 + z0))), hi(__bfloat162bfloat162(__int2bfloat16_rn(128 + z1))) {}
+};
+
+// Eight codes of one word to the fragment q - z, exact: a nibble put under the
+// bits of 1024 is 1024 + q (fp16, nibbles 0 and 4) or 1024 + 16 q (nibbles 1
+// and 5), and the subtraction, or the fused multiply by 1/16 and subtraction,
+// rounds nothing.  bf16 has 7 mantissa bits: a nibble under 128 is 128 + q.
+__device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__half>& z, uint32_t (&a)[4]) {
+  const uint32_t base = 0x64006400u;
+  const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));
+  const uint32_t v = w >> 8;
+  union U {
+    uint32_t u;
+    __half2 h;
+  } x;
+  x.u = and_or(w, 0x000F000Fu, base);
+  x.h = __hsub2(x.h, z.lo);
+  a[0] = x.u;
+  x.u = and_or(w, 0x00F000F0u, base);
+  x.h = __hfma2(x.h, sixteenth, z.hi);
+  a[1] = x.u;
+  x.u = and_or(v, 0x000F000Fu, base);
+  x.h = __hsub2(x.h, z.lo);
+  a[2] = x.u;
+  x.u = and_or(v, 0x00F000F0u, base);
+  x.h = __hfma2(x.h, sixteenth, z.hi);
+  a[3] = x.u;
+}
+__device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__nv_bfloat16>& z, uint32_t (&a)[4]) {
+  const uint32_t base = 0x43004300u;
+  union U {
+    uint32_t u;
+    __nv_bfloat162 h;
+  } x;
+  x.u = and_or(w, 0x000F000Fu, base);
+  x.h = __hsub2(x.h, z.lo);
+  a[0] = x.u;
+  x.u = and_or(w >> 4, 0x000F000Fu, base);
+  x.h = __hsub2(x.h, z.hi);
+  a[1] = x.u;
+  x.u = and_or(w >> 8, 0x000F000Fu, base);
+  x.h = __hsub2(x.h, z.lo);
+  a[2] = x.u;
+  x.u = and_or(w >> 12, 0x000F000Fu, base);
+  x.h = __hsub2(x.h, z.hi);
+  a[3] = x.u;
+}
+
+// c += a (16 x 16) * b (16 x 8), fp32 sums.
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- loads
+
+// Codes are read once: keep them out of L1, where the activations live.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Eight activations k .. k + 7 of one row as four fragment words, zero past K.
+// Vec: the row starts on 16 bytes and holds a multiple of 8 values.
+template <bool Vec>
+__device__ __forceinline__ uint4 load_act8(const uint16_t* row, int32_t k, int32_t K) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (Vec) {
+    if (row && k < K) v = *reinterpret_cast<const uint4*>(row + k);
+  } else if (row) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < K) w[i >> 1] |= static_cast<uint32_t>(row[k + i]) << (16 * (i & 1));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+// Scales and zero points of one unit as a lane needs them (NG groups a unit).
+template <typename T, int NG>
+struct W4Groups {
+  uint32_t s[NG];  // {row g, row g + 8} in 16 bits each
+  uint32_t z[NG];  // {row g, row g + 8} in 8 bits each
+
+  __device__ __forceinline__ void load(const W4Dev& A, int64_t unit, int g) {
+    const int64_t at = (unit * 8 + g) * (NG * 2);
+    const uint16_t* sp = A.scales + at;
+    if (NG == 1) {
+      s[0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
+    } else if (NG == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+      s[0] = v.x;
+      s[NG - 1] = v.y;
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+      s[0] = v.x;
+      s[1 % NG] = v.y;
+      s[2 % NG] = v.z;
+      s[NG - 1] = v.w;
+    }
+    if (A.zeros) {
+      const uint8_t* zp = A.zeros + at;
+      if (NG == 1) {
+        z[0] = __ldg(reinterpret_cast<const uint16_t*>(zp));
+      } else if (NG == 2) {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(zp));
+        z[0] = v & 0xFFFF;
+        z[NG - 1] = v >> 16;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(zp));
+        z[0] = v.x & 0xFFFF;
+        z[1 % NG] = v.x >> 16;
+        z[2 % NG] = v.y & 0xFFFF;
+        z[NG - 1] = v.y >> 16;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) z[i] = 0x0808u;
+    }
+  }
+  __device__ __forceinline__ float scale(int i, int row) const {
+    return bits_to_float<T>(static_cast<uint16_t>(row ? s[i] >> 16 : s[i] & 0xFFFF));
+  }
+  __device__ __forceinline__ int zero_point(int i, int row) const {
+    return static_cast<int>(row ? z[i] >> 8 : z[i] & 0xFF);
+  }
+  __device__ __forceinline__ W4Zero<T> zero(int i) const { return W4Zero<T>(zero_point(i, 0), zero_point(i, 1)); }
+};
+
+// One unit of R strips times NT * 8 activation rows: acc[r][nt] += s * ((q - z) x B).
+// `act(nt, k)` gives the lane's 16 bytes of activations k .. k + 7 of row
+// 8 * nt + g (zeros where there is none); tiles from `tiles` on are skipped.
+// A group is multiplied as whole numbers q - z and scaled in fp32 afterwards,
+// so a weight is never rounded.
+template <typename T, int NG, int R, int NT, typename Act>
+__device__ __forceinline__ void w4_unit(const uint4 (&c)[R][2], const W4Groups<T, NG> (&grp)[R], int32_t k0, int tiles,
+                                        const Act& act, float (&acc)[R][NT][4]) {
+  constexpr int kBlocks = 4 / NG;
+#pragma unroll
+  for (int gi = 0; gi < NG; ++gi) {
+    uint32_t a[R][2 * kBlocks][4];
+    float s0[R], s1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const W4Zero<T> z = grp[r].zero(gi);
+      s0[r] = grp[r].scale(gi, 0);
+      s1[r] = grp[r].scale(gi, 1);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const int blk = gi * kBlocks + b;
+        const uint4 v = c[r][blk >> 1];
+        w4_fragment(blk & 1 ? v.z : v.x, z, a[r][2 * b]);
+        w4_fragment(blk & 1 ? v.w : v.y, z, a[r][2 * b + 1]);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt >= tiles) break;
+      uint4 x[kBlocks];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) x[b] = act(nt, k0 + 32 * (gi * kBlocks + b));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          mma16816<T>(d, a[r][2 * b], x[b].x, x[b].y);
+          mma16816<T>(d, a[r][2 * b + 1], x[b].z, x[b].w);
+        }
+        acc[r][nt][0] = fmaf(s0[r], d[0], acc[r][nt][0]);
+        acc[r][nt][1] = fmaf(s0[r], d[1], acc[r][nt][1]);
+        acc[r][nt][2] = fmaf(s1[r], d[2], acc[r][nt][2]);
+        acc[r][nt][3] = fmaf(s1[r], d[3], acc[r][nt][3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launchers
+
+cudaError_t launch_w4_encode(const void* W, int64_t ldw, const flashspmm_w4* A, int symmetric, cudaStream_t s);
+cudaError_t launch_w4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros, const flashspmm_w4* A,
+                           cudaStream_t s);
+cudaError_t launch_w4_decode(const flashspmm_w4* A, void* W, bool f32, cudaStream_t s);
+
+// Activations whose rows do not start on 16 bytes, or whose length is not a
+// multiple of 8, are copied first: rows x K values to rows of aligned_k(K)
+// values, zero behind K.
+inline int64_t aligned_k(int32_t K) { return (static_cast<int64_t>(K) + 7) / 8 * 8; }
+bool rows_aligned(const void* X, int64_t ld, int32_t K);
+cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K, void* out, cudaStream_t s);
+
+size_t w4_matmul_workspace(int32_t M, int32_t K, int32_t N, bool aligned);
+cudaError_t launch_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
+                             int32_t N, void* workspace, cudaStream_t s);
+
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxTopK = 16;
+
+struct MoeCall {
+  flashspmm_w4 gate, up, down;  // up.codes null: no gate product
+  const void* X;
+  int64_t ldx;
+  const void* router;  // null: ids and weights are inputs
+  int32_t router_dtype;
+  int32_t tokens, top_k;
+  bool renormalize;
+  int32_t activation;
+  int32_t* ids;
+  float* weights;
+  void* out;
+  int64_t ldo;
+};
+size_t moe_workspace(int32_t T, int32_t E, int32_t top_k, int32_t H, int32_t F, bool aligned);
+cudaError_t launch_moe_w4(const MoeCall& p, void* workspace, cudaStream_t s);
+
+}  // namespace flashspmm

@@ -1,0 +1,327 @@
+"""4-bit weights with group scales: encoder, skinny product and the
+mixture-of-experts layer (argument marshalling only; see "4-bit weights" in
+``include/flashspmm.h``).
+
+A weight is ``w = s * (q - z)`` with codes q in 0..15, one scale s (float16 or
+bfloat16) and, unless it is symmetric, one zero point z for each group of 32,
+64 or 128 neighbours along K.  Activations have the scales' type.
+
+Every call runs on the device of its tensors.  ``stream`` is a
+``torch.cuda.Stream``, a raw handle or None for the current stream of that
+device; outputs and scratch are allocated on the stream the call runs on, so
+calls on different streams share nothing and every call can be captured in a
+CUDA graph.  Inputs made on another stream are ordered by the caller, as with
+torch's own operators.  These are inference calls: an input that requires
+grad is refused while grad mode is on.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass, field
+
+import torch
+
+from . import binding
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
+
+
+class _W4View(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("count", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
+@dataclass(frozen=True, eq=False)
+class W4:
+    """A 4-bit matrix [M, K], or a stack [count, M, K], in device memory."""
+    codes: torch.Tensor          # uint8 [count, strips, units, 1024]
+    scales: torch.Tensor         # float16 or bfloat16 [count, strips, units, 8, 128 // group, 2]
+    zeros: torch.Tensor | None   # uint8, the scales' shape; None: every zero point is 8
+    M: int
+    K: int
+    group: int
+    stacked: bool = False        # made from a 3-D tensor
+    _ref: object = field(default=None, init=False, repr=False)
+
+    def __post_init__(self):
+        z = self.zeros
+        v = _W4View(self.M, self.K, self.codes.shape[0], self.group, _DTYPES[self.scales.dtype], 0,
+                    self.codes.data_ptr() or None, self.scales.data_ptr() or None,
+                    None if z is None else z.data_ptr() or None)
+        object.__setattr__(self, "_ref", ctypes.byref(v))  # byref keeps the structure alive
+
+    @property
+    def count(self) -> int:
+        return int(self.codes.shape[0])
+
+    @property
+    def dtype(self) -> torch.dtype:
+        return self.scales.dtype
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.zeros) if t is not None)
+
+    def matrix(self, index: int) -> "W4":
+        """One matrix of a stack as a view; nothing is copied."""
+        if not 0 <= index < self.count:
+            raise IndexError(f"matrix {index} of a stack of {self.count}")
+        part = slice(index, index + 1)
+        return W4(self.codes[part], self.scales[part], None if self.zeros is None else self.zeros[part], self.M,
+                  self.K, self.group)
+
+
+class _On:
+    """Makes a tensor's device and the stream that a caller named current."""
+
+    def __init__(self, device: torch.device, stream):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+                torch.cuda.default_stream(device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self._device, self._stream = torch.cuda.device(device), torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._device.__enter__()
+        self._stream.__enter__()
+
+    def __exit__(self, *exc):
+        self._stream.__exit__(*exc)
+        self._device.__exit__(*exc)
+
+
+def _elsewhere(device: torch.device, stream) -> bool:
+    return stream is not None or torch.cuda.current_device() != device.index
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _scratch(nbytes: int, device: torch.device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _cuda(t, name: str, dtypes) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA tensor of type " + " or ".join(str(d) for d in dtypes))
+
+
+def _no_grad(*tensors) -> None:
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError("4-bit weights have no backward pass: call this under torch.no_grad()")
+
+
+def _rows(t: torch.Tensor) -> tuple:
+    """A 2-D tensor with unit stride along its rows, and the distance of its rows."""
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        t = t.contiguous()
+    return t, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _output(t, shape: tuple, dtypes, device: torch.device, name: str) -> int:
+    """Checks an output that the caller gave; the distance of its rows."""
+    _cuda(t, name, dtypes)
+    if t.shape != shape or t.device != device or (shape[1] > 1 and t.stride(1) != 1) or \
+            (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must be a {list(shape)} tensor on {device} with unit stride along its rows")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _empty(shape, dtype: torch.dtype, group: int, symmetric: bool, device: torch.device) -> W4:
+    """Unwritten buffers for a weight of shape [M, K] or [count, M, K]."""
+    lib = binding.load_library()
+    count, (M, K) = (shape[0] if len(shape) == 3 else 1), shape[-2:]
+    if lib.flashspmm_w4_sizes(M, K, count, group, None, None, None) != 0:
+        raise ValueError(f"4-bit weights need group 32, 64 or 128 and at least one matrix, got group {group}, "
+                         f"shape {tuple(shape)}")
+    strips, units = -(-M // 16), -(-K // 128)
+    per = (count, strips, units, 8, 128 // group, 2)
+    return W4(torch.empty((count, strips, units, 1024), dtype=torch.uint8, device=device),
+              torch.empty(per, dtype=dtype, device=device),
+              None if symmetric else torch.empty(per, dtype=torch.uint8, device=device), M, K, group, len(shape) == 3)
+
+
+def w4_encode(W: torch.Tensor, group: int = 128, symmetric: bool = True, stream=None) -> W4:
+    """Quantise a dense float16 or bfloat16 weight ``[M, K]`` (or a stack
+    ``[count, M, K]``) on the GPU: symmetric codes around 8, or asymmetric
+    ones with a zero point per group."""
+    _cuda(W, "W", (torch.float16, torch.bfloat16))
+    if W.dim() not in (2, 3):
+        raise TypeError("W must have 2 or 3 dimensions")
+    _no_grad(W)
+    if _elsewhere(W.device, stream):
+        with _On(W.device, stream):
+            return w4_encode(W, group, symmetric)
+    if W.dim() == 3:
+        rows, ldw = W.contiguous(), W.shape[2]
+    else:
+        rows, ldw = _rows(W)
+    A = _empty(W.shape, W.dtype, group, symmetric, W.device)
+    binding._check(binding.load_library().flashspmm_w4_encode(rows.data_ptr() or None, ldw, int(symmetric), A._ref,
+                                                              _raw_stream(W.device)), "w4_encode")
+    return A
+
+
+def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, group: int = 128,
+            stream=None) -> W4:
+    """Lay out codes quantised elsewhere: uint8 ``codes`` ``[M, K]`` (or
+    ``[count, M, K]``) of 0..15, ``scales`` and uint8 ``zeros`` (0..127; None =
+    all 8) of ``[M, ceil(K / group)]`` (or with count)."""
+    _cuda(codes, "codes", (torch.uint8, ))
+    _cuda(scales, "scales", (torch.float16, torch.bfloat16))
+    if codes.dim() not in (2, 3):
+        raise TypeError("codes must have 2 or 3 dimensions")
+    _no_grad(scales)
+    if _elsewhere(codes.device, stream):
+        with _On(codes.device, stream):
+            return w4_pack(codes, scales, zeros, group)
+    A = _empty(codes.shape, scales.dtype, group, zeros is None, codes.device)
+    per = (*codes.shape[:-1], -(-codes.shape[-1] // group))
+    if zeros is not None:
+        _cuda(zeros, "zeros", (torch.uint8, ))
+    for name, t in (("scales", scales), ("zeros", zeros)):
+        if t is not None and (t.shape != per or t.device != codes.device):
+            raise ValueError(f"{name} must be a {list(per)} tensor on {codes.device}")
+    codes, scales, zeros = codes.contiguous(), scales.contiguous(), None if zeros is None else zeros.contiguous()
+    binding._check(binding.load_library().flashspmm_w4_pack(
+        codes.data_ptr() or None, scales.data_ptr() or None, None if zeros is None else zeros.data_ptr() or None,
+        A._ref, _raw_stream(codes.device)), "w4_pack")
+    return A
+
+
+def w4_decode(A: W4, dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """The dense weight ``s * (q - z)`` in A's type (rounded once) or, with
+    ``dtype=torch.float32``, exactly."""
+    dtype = A.dtype if dtype is None else dtype
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be the weight's own or torch.float32")
+    if _elsewhere(A.device, stream):
+        with _On(A.device, stream):
+            return w4_decode(A, dtype)
+    shape = (A.count, A.M, A.K) if A.stacked else (A.M, A.K)
+    W = torch.empty(shape, dtype=dtype, device=A.device)
+    binding._check(binding.load_library().flashspmm_w4_decode(A._ref, W.data_ptr() or None, _DTYPES[dtype],
+                                                              _raw_stream(A.device)), "w4_decode")
+    return W
+
+
+def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """C = A x B for a skinny B.  B is ``[N, K]`` in A's type with N = 1..256
+    (rows may be apart); returns C as ``[N, M]`` in that type, or writes the
+    given C, which may be float32 (the unrounded sums)."""
+    lib = binding._lib or binding.load_library()
+    device, dtype = A.codes.device, A.scales.dtype
+    if B.dtype is not dtype or B.dim() != 2 or B.device != device:
+        raise TypeError(f"B must be a 2-D {dtype} tensor on {device}")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return w4_matmul(A, B, C)
+    _no_grad(B)
+    if B.shape[1] != A.K:
+        raise ValueError(f"B has shape {tuple(B.shape)}, expected (N, {A.K})")
+    B, ldb = _rows(B)
+    N = B.shape[0]
+    if C is None:
+        C, ldc = torch.empty((N, A.M), dtype=dtype, device=device), A.M
+    else:
+        ldc = _output(C, (N, A.M), (dtype, torch.float32), device, "C")
+    ptr = B.data_ptr()
+    need = lib.flashspmm_w4_matmul_workspace_bytes(A._ref, ptr, ldb, N)
+    ws = _scratch(need, device)
+    status = lib.flashspmm_w4_matmul(A._ref, ptr, ldb, C.data_ptr(), ldc, _DTYPES[C.dtype], N,
+                                     None if ws is None else ws.data_ptr(), need, _raw_stream(device))
+    if status:
+        binding._check(status, "w4_matmul")
+    return C
+
+
+def _moe(X, router, gate, up, down, top_k, renormalize, activation, ids, weights, out):
+    lib = binding._lib or binding.load_library()
+    device, dtype = gate.codes.device, gate.scales.dtype
+    X, ldx = _rows(X)
+    T = X.shape[0]
+    if out is None:
+        out, ldo = torch.empty((T, gate.K), dtype=dtype, device=device), gate.K
+    else:
+        ldo = _output(out, (T, gate.K), (dtype, ), device, "out")
+    ptr = X.data_ptr()
+    need = lib.flashspmm_moe_w4_workspace_bytes(gate._ref, ptr, ldx, T, top_k)
+    ws = _scratch(need, device)
+    status = lib.flashspmm_moe_w4(
+        gate._ref, None if up is None else up._ref, down._ref, ptr, ldx, None if router is None else router.data_ptr(),
+        _DTYPES[dtype if router is None else router.dtype], T, top_k, renormalize, activation, ids.data_ptr(),
+        weights.data_ptr(), out.data_ptr(), ldo, None if ws is None else ws.data_ptr(), need, _raw_stream(device))
+    if status:
+        binding._check(status, "moe_w4")
+    return out
+
+
+def _check_experts(X, gate: W4, up, down: W4, activation: str) -> None:
+    device, dtype = gate.codes.device, gate.scales.dtype
+    if X.dtype is not dtype or X.dim() != 2 or X.device != device:
+        raise TypeError(f"X must be a 2-D {dtype} tensor on {device}")
+    if X.shape[1] != gate.K:
+        raise ValueError(f"X has shape {tuple(X.shape)}, expected (T, {gate.K})")
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be one of " + ", ".join(_ACTIVATIONS))
+    for w in (up, down):
+        if w is not None and w.codes.device != device:
+            raise ValueError("the experts' weights must be on one device")
+
+
+def moe_w4(X: torch.Tensor, router: torch.Tensor, gate: W4, up: W4 | None, down: W4, top_k: int,
+           renormalize: bool = True, activation: str = "silu", out: torch.Tensor | None = None, stream=None) -> tuple:
+    """A mixture-of-experts layer for T = 1..64 tokens: ``(out, ids, weights)``.
+
+    X        ``[T, H]``;  router  ``[E, H]`` in X's type or float32.
+    gate, up stacks ``[E, F, H]`` (``up=None``: no gate product);  down  ``[E, H, F]``.
+    The token's ``top_k`` experts (ties to the lower index) are weighted with
+    the softmax over their logits (``renormalize``) or over all logits, and
+    ``out = sum weights * down(act(gate x) * up x)``.  ``activation`` is
+    "silu", "gelu" (with erf) or "relu".  ``ids`` is int32 and ``weights``
+    float32, both ``[T, top_k]``, the largest first."""
+    _check_experts(X, gate, up, down, activation)
+    device = gate.codes.device
+    if (router.dtype is not X.dtype and router.dtype is not torch.float32) or router.device != device or \
+            router.shape != (gate.codes.shape[0], gate.K):
+        raise TypeError(f"router must be a [{gate.count}, {gate.K}] tensor of X's type or float32 on {device}")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return moe_w4(X, router, gate, up, down, top_k, renormalize, activation, out)
+    _no_grad(X, router)
+    ids = torch.empty((X.shape[0], top_k), dtype=torch.int32, device=device)
+    weights = torch.empty((X.shape[0], top_k), dtype=torch.float32, device=device)
+    out = _moe(X, router.contiguous(), gate, up, down, top_k, int(renormalize), _ACTIVATIONS[activation], ids, weights,
+               out)
+    return out, ids, weights
+
+
+def moe_w4_experts(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: W4, up: W4 | None, down: W4,
+                   activation: str = "silu", out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts of ``moe_w4`` under the caller's own routing: int32 ``ids``
+    and float32 ``weights`` of ``[T, top_k]``.  An id outside 0..E-1 (padding,
+    or an expert of another rank) contributes nothing; a token whose ids are
+    all outside gets zeros."""
+    _check_experts(X, gate, up, down, activation)
+    device = gate.codes.device
+    _cuda(ids, "ids", (torch.int32, ))
+    _cuda(weights, "weights", (torch.float32, ))
+    if ids.dim() != 2 or ids.shape[0] != X.shape[0] or weights.shape != ids.shape or ids.device != device or \
+            weights.device != device:
+        raise ValueError(f"ids and weights must be [T, top_k] tensors on {device}")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return moe_w4_experts(X, ids, weights, gate, up, down, activation, out)
+    _no_grad(X, weights)
+    return _moe(X, None, gate, up, down, ids.shape[1], 1, _ACTIVATIONS[activation], ids.contiguous(),
+                weights.contiguous(), out)

@@ -65,12 +65,8 @@ void matmul_as(const W4Dev& A, const uint16_t* B, int64_t ldb, void* C, int64_t 
       A, B, ldb, C, ldc, c_f32, N)
   if (N <= 8)
     FLASHSPMM_MATMUL(2, 1);
-  else if (N <= 16)
-    FLASHSPMM_MATMUL(2, 2);
-  else if (N <= 32)
-    FLASHSPMM_MATMUL(2, 4);
   else
-    FLASHSPMM_MATMUL(1, 8);
+    FLASHSPMM_MATMUL(2, 2);
 #undef FLASHSPMM_MATMUL
 }
 
@@ -97,11 +93,13 @@ cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K
 }
 
 size_t w4_matmul_workspace(int32_t, int32_t K, int32_t N, bool aligned) {
+  if (N > kW4FragmentTokens) return w4_gemm_workspace(K, N);
   return aligned ? 0 : static_cast<size_t>(N) * aligned_k(K) * 2;
 }
 
 cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                              int32_t N, void* workspace, cudaStream_t s) {
+  if (N > kW4FragmentTokens) return launch_w4_gemm(in, B, ldb, C, ldc, c_f32, N, workspace, s);
   W4Dev A = w4_dev(in);
   if (!rows_aligned(B, ldb, A.K)) {
     const cudaError_t e = launch_align_rows(B, ldb, N, A.K, workspace, s);

@@ -401,7 +401,7 @@ flashspmm_status flashspmm_w4_encode(const void* W, int64_t ldw, int32_t symmetr
 /* Lays out codes that the caller has (a checkpoint quantised elsewhere).
  *   codes   device uint8[count * M][K], one code each, the low 4 bits are used.
  *   scales  device, A->dtype, [count * M][ceil(K / group)].
- *   zeros   device uint8 of the same shape, 0..127 (the low 7 bits are used);
+ *   zeros   device uint8 of the same shape, 0..63 (the low 6 bits are used);
  *           NULL if and only if A->zeros is NULL. */
 flashspmm_status flashspmm_w4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros,
                                    const flashspmm_w4* A, void* stream);

@@ -174,7 +174,8 @@ def test_matmul(dtype, group, symmetric, N):
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 129, 3), (15, 7, 8), (16, 128, 1), (17, 8, 256), (129, 257, 17),
-                                   (4099, 5003, 17), (128, 36864, 5), (320, 49152, 70), (9216, 64, 1), (2048, 2048, 40)])
+                                   (4099, 5003, 17), (128, 36864, 5), (20000, 640, 256), (1280, 24576, 256),
+                                   (1280, 24576, 200), (20000, 640, 144), (2600, 24576, 24), (320, 49152, 70), (9216, 64, 1), (2048, 2048, 40)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_matmul_whole_numbers_are_exact(M, K, N, dtype):
     codes, scales, zeros = codes_of((M, K), 64, dtype, False, 7, whole=True)

@@ -99,15 +99,17 @@ template <typename T>
 struct W4Zero;
 template <>
 struct W4Zero<__half> {
-  __half2 lo, hi;  // 1024 + z, -(64 + z')
+  __half2 lo, hi;  // 1024 + z, -(64 + z'), put together as bits: steps there are 1 and 1/16, and z < 64
   __device__ __forceinline__ W4Zero(int z0, int z1)
-      : lo(__half2half2(__int2half_rn(1024 + z0))), hi(__half2half2(__int2half_rn(-64 - z1))) {}
+      : lo(__half2half2(__ushort_as_half(static_cast<uint16_t>(0x6400 | z0)))),
+        hi(__half2half2(__ushort_as_half(static_cast<uint16_t>(0xD400 | (z1 << 4))))) {}
 };
 template <>
 struct W4Zero<__nv_bfloat16> {
   __nv_bfloat162 lo, hi;  // 128 + z, 128 + z'
   __device__ __forceinline__ W4Zero(int z0, int z1)
-      : lo(__bfloat162bfloat162(__int2bfloat16_rn(128 + z0))), hi(__bfloat162bfloat162(__int2bfloat16_rn(128 + z1))) {}
+      : lo(__bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(0x4300 | z0)))),
+        hi(__bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(0x4300 | z1)))) {}
 };
 
 // Eight codes of one word to the fragment q - z, exact: a nibble put under the
@@ -322,7 +324,7 @@ cudaError_t launch_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, 
 
 // The same product by tcgen05 (w4_gemm.cu), for N > kW4FragmentTokens.
 constexpr int kW4FragmentTokens = 16;
-size_t w4_gemm_workspace(int32_t K, int32_t N);
+size_t w4_gemm_workspace(int32_t M, int32_t K, int32_t N);
 cudaError_t launch_w4_gemm(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                            int32_t N, void* workspace, cudaStream_t s);
 

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32) w4_pack_kernel(const uint8_t* __r
         const bool have = ok && g0 + gi < groups;
         const int64_t src = (at.row + 8 * r) * groups + g0 + gi;
         sc[r][gi] = have ? in_scales[src] : 0u;
-        zp[r][gi] = have && in_zeros ? in_zeros[src] & 0x7Fu : 8u;
+        zp[r][gi] = have && in_zeros ? in_zeros[src] & 0x3Fu : 8u;
       }
     }
     uint32_t words[8];

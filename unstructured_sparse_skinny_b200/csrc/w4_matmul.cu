@@ -92,8 +92,8 @@ cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K
   return cudaGetLastError();
 }
 
-size_t w4_matmul_workspace(int32_t, int32_t K, int32_t N, bool aligned) {
-  if (N > kW4FragmentTokens) return w4_gemm_workspace(K, N);
+size_t w4_matmul_workspace(int32_t M, int32_t K, int32_t N, bool aligned) {
+  if (N > kW4FragmentTokens) return w4_gemm_workspace(M, K, N);
   return aligned ? 0 : static_cast<size_t>(N) * aligned_k(K) * 2;
 }
 

@@ -175,7 +175,7 @@ def w4_encode(W: torch.Tensor, group: int = 128, symmetric: bool = True, stream=
 def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, group: int = 128,
             stream=None) -> W4:
     """Lay out codes quantised elsewhere: uint8 ``codes`` ``[M, K]`` (or
-    ``[count, M, K]``) of 0..15, ``scales`` and uint8 ``zeros`` (0..127; None =
+    ``[count, M, K]``) of 0..15, ``scales`` and uint8 ``zeros`` (0..63; None =
     all 8) of ``[M, ceil(K / group)]`` (or with count)."""
     _cuda(codes, "codes", (torch.uint8, ))
     _cuda(scales, "scales", (torch.float16, torch.bfloat16))

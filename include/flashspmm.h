@@ -363,12 +363,12 @@ enum { FLASHSPMM_ACT_SILU = 0, FLASHSPMM_ACT_GELU = 1, FLASHSPMM_ACT_RELU = 2 };
  * weight).  The buffers are the caller's, of flashspmm_w4_sizes bytes, written
  * by flashspmm_w4_encode or flashspmm_w4_pack.
  *
- * Layout: strips of 16 rows times units of 128 columns, both padded with zero
- * weights; unit (matrix, strip, u) takes 1024 bytes of codes at
- * ((matrix * ceil(M/16) + strip) * ceil(K/128) + u) * 1024, ordered so that
- * lane 4 g + t of a warp finds the codes of its tensor-core fragments (rows g
- * and g + 8, columns 32 b + 8 t .. + 7 of each 32-column block b) in two
- * 16-byte loads.  Scales and zero points of a unit are
+ * Layout: blocks of 128 rows (eight strips of 16) times units of 128 columns,
+ * both padded with zero weights; the unit of one strip takes 1024 bytes of
+ * codes at (((matrix * ceil(M/128) + block) * ceil(K/128) + unit) * 8 + strip)
+ * * 1024, ordered so that lane 4 g + t of a warp finds the codes of its
+ * tensor-core fragments (rows g and g + 8, columns 32 b + 8 t .. + 7 of each
+ * 32-column block b) in two 16-byte loads.  Its scales and zero points are
  * [8][128 / group][2] entries: [g][group][row g, row g + 8]. */
 typedef struct {
   int32_t M, K;          /* rows and columns of one matrix, each <= 2^30 */

@@ -28,7 +28,8 @@ def view(**kw):
 
 
 @pytest.mark.parametrize("M,K,count,group,units", [
-    (16, 128, 1, 128, 1), (17, 129, 1, 64, 4), (1, 1, 3, 32, 3), (0, 128, 1, 128, 0), (4099, 5003, 2, 32, 2 * 257 * 40),
+    (16, 128, 1, 128, 8), (129, 129, 1, 64, 32), (1, 1, 3, 32, 24), (0, 128, 1, 128, 0),
+    (4099, 5003, 2, 32, 2 * 33 * 8 * 40),
     (1 << 20, 1 << 20, 4, 128, 4 * (1 << 16) * (1 << 13)),
 ])
 def test_sizes(lib, M, K, count, group, units):

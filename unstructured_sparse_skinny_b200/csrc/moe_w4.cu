@@ -294,11 +294,10 @@ __global__ void __launch_bounds__(kWarps * 32) moe_gate_up_kernel(W4Dev gate, W4
     const int n = 8 * nt + g;
     return load_act8<true>(n < slot.count ? X + tok[n] * ldx : nullptr, k + 8 * t, H);
   };
-  const int64_t strip = static_cast<int64_t>(slot.expert) * gate.strips + blockIdx.x;
   for (int32_t u = warp; u < gate.units; u += kWarps) {
     uint4 c[R][2];
     W4Groups<T, NG> grp[R];
-    const int64_t unit = strip * gate.units + u;
+    const int64_t unit = gate.unit(slot.expert, blockIdx.x, u);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const W4Dev& A = r ? up : gate;
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(kWarps * 32) moe_down_kernel(W4Dev A, int32_t 
     const Slot slot = ws.slots[s];
     const int64_t stop = min64(end, static_cast<int64_t>(s + 1) * A.units);
     const int tiles = (slot.count + 7) / 8;
-    const int64_t strip = (static_cast<int64_t>(slot.expert) * A.strips + blockIdx.x) * A.units;
+    const int64_t unit0 = A.unit(slot.expert, blockIdx.x, 0);
     float acc[1][NT][4] = {};
     const auto act = [&](int nt, int32_t k) {
       const int n = 8 * nt + g;
@@ -370,9 +369,10 @@ __global__ void __launch_bounds__(kWarps * 32) moe_down_kernel(W4Dev A, int32_t 
       const int32_t u = static_cast<int32_t>(i - static_cast<int64_t>(s) * A.units);
       uint4 c[1][2];
       W4Groups<T, NG> grp[1];
-      c[0][0] = ld_stream(A.codes + (strip + u) * 64 + lane);
-      c[0][1] = ld_stream(A.codes + (strip + u) * 64 + 32 + lane);
-      grp[0].load(A, strip + u, g);
+      const int64_t unit = unit0 + 8 * static_cast<int64_t>(u);
+      c[0][0] = ld_stream(A.codes + unit * 64 + lane);
+      c[0][1] = ld_stream(A.codes + unit * 64 + 32 + lane);
+      grp[0].load(A, unit, g);
       w4_unit<T, NG, 1, NT>(c, grp, u * kW4UnitCols, tiles, act, acc);
     }
 #pragma unroll

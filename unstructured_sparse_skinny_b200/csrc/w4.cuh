@@ -1,9 +1,11 @@
 // 4-bit weights with group scales: layout, launchers and the warp-level
 // product shared by the skinny matrix product and the experts' products.
 //
-// Layout.  A matrix of M x K codes is cut into strips of 16 rows and units of
-// 128 columns; unit (strip, u) is 1024 bytes at (strip * units + u) * 1024.
-// A warp reads it with two 16-byte loads per lane, and every lane then holds
+// Layout.  A matrix of M x K codes is cut into strips of 16 rows, eight strips
+// to a block of 128, and units of 128 columns.  A unit of one strip takes 1024
+// bytes; the eight of a block follow one another, then come the block's next
+// 128 columns, so a block's unit is one copy for the large-batch kernel.  A
+// warp reads a unit of a strip with two 16-byte loads per lane, and every lane then holds
 // exactly the codes of its own mma.m16n8k16 A fragments, so nothing is
 // shuffled or staged.  Lane l = 4 * g + t owns rows g and g + 8 and, in each
 // 32-column block b of the unit, the eight columns 32 * b + 8 * t .. + 7.  The
@@ -38,13 +40,22 @@ struct W4Dev {
   const uint16_t* scales;
   const uint8_t* zeros;  // nullptr: every zero point is 8
   int32_t M, K;
-  int32_t strips;  // of one matrix
+  int32_t strips;  // of one matrix that hold rows (the layout pads them to whole blocks)
+  int32_t blocks;  // of one matrix
   int32_t units;   // of one strip
   int32_t group;
+
+  // Number of unit u of a strip; its next unit is 8 further on.
+  __device__ __forceinline__ int64_t unit(int64_t matrix, int32_t strip, int32_t u) const {
+    return ((matrix * blocks + (strip >> 3)) * units + u) * 8 + (strip & 7);
+  }
 };
 
 __host__ __device__ inline int32_t w4_strips(int32_t M) {
   return static_cast<int32_t>((static_cast<int64_t>(M) + kW4StripRows - 1) / kW4StripRows);
+}
+__host__ __device__ inline int32_t w4_blocks(int32_t M) {
+  return static_cast<int32_t>((static_cast<int64_t>(M) + 127) / 128);
 }
 __host__ __device__ inline int32_t w4_units(int32_t K) {
   return static_cast<int32_t>((static_cast<int64_t>(K) + kW4UnitCols - 1) / kW4UnitCols);
@@ -58,6 +69,7 @@ inline W4Dev w4_dev(const flashspmm_w4* A) {
   d.M = A->M;
   d.K = A->K;
   d.strips = w4_strips(A->M);
+  d.blocks = w4_blocks(A->M);
   d.units = w4_units(A->K);
   d.group = A->group;
   return d;
@@ -212,30 +224,31 @@ struct W4Groups {
 
   __device__ __forceinline__ void load(const W4Dev& A, int64_t unit, int g) {
     const int64_t at = (unit * 8 + g) * (NG * 2);
-    const uint16_t* sp = A.scales + at;
+    load(A.scales + at, A.zeros ? A.zeros + at : nullptr);
+  }
+  __device__ __forceinline__ void load(const uint16_t* sp, const uint8_t* zp) {
     if (NG == 1) {
-      s[0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
+      s[0] = *reinterpret_cast<const uint32_t*>(sp);
     } else if (NG == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+      const uint2 v = *reinterpret_cast<const uint2*>(sp);
       s[0] = v.x;
       s[NG - 1] = v.y;
     } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+      const uint4 v = *reinterpret_cast<const uint4*>(sp);
       s[0] = v.x;
       s[1 % NG] = v.y;
       s[2 % NG] = v.z;
       s[NG - 1] = v.w;
     }
-    if (A.zeros) {
-      const uint8_t* zp = A.zeros + at;
+    if (zp) {
       if (NG == 1) {
-        z[0] = __ldg(reinterpret_cast<const uint16_t*>(zp));
+        z[0] = *reinterpret_cast<const uint16_t*>(zp);
       } else if (NG == 2) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(zp));
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(zp);
         z[0] = v & 0xFFFF;
         z[NG - 1] = v >> 16;
       } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(zp));
+        const uint2 v = *reinterpret_cast<const uint2*>(zp);
         z[0] = v.x & 0xFFFF;
         z[1 % NG] = v.x >> 16;
         z[2 % NG] = v.y & 0xFFFF;

@@ -44,7 +44,7 @@ extern "C" {
 int flashspmm_w4_sizes(int32_t M, int32_t K, int32_t count, int32_t group, int64_t* codes_bytes, int64_t* scales,
                        int64_t* zeros) {
   if (check_shape(M, K, count, group) != FLASHSPMM_OK) return -1;
-  const int64_t units = static_cast<int64_t>(count) * w4_strips(M) * w4_units(K);
+  const int64_t units = static_cast<int64_t>(count) * w4_blocks(M) * 8 * w4_units(K);
   const int64_t groups = units * kW4StripRows * (kW4UnitCols / group);
   if (codes_bytes) *codes_bytes = units * kW4UnitBytes;
   if (scales) *scales = groups;

@@ -54,10 +54,10 @@ struct Place {
   bool ok0, ok1;    // rows g and g + 8 exist
   int32_t col0;     // first column of block 0 for this lane
   __device__ __forceinline__ Place(const W4Dev& A, int64_t unit, int lane) {
-    const int64_t strip = unit / A.units;
-    const int32_t u = static_cast<int32_t>(unit - strip * A.units);
-    const int64_t mat = strip / A.strips;
-    const int64_t r = (strip - mat * A.strips) * kW4StripRows + (lane >> 2);
+    const int64_t part = unit >> 3, block = part / A.units;
+    const int32_t u = static_cast<int32_t>(part - block * A.units);
+    const int64_t mat = block / A.blocks;
+    const int64_t r = ((block - mat * A.blocks) * 8 + (unit & 7)) * kW4StripRows + (lane >> 2);
     row = mat * A.M + r;
     ok0 = r < A.M;
     ok1 = r + 8 < A.M;
@@ -324,7 +324,7 @@ void decode_as(const W4Dev& A, O* W, bool vec, int64_t total, cudaStream_t s) {
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int64_t all_units(const flashspmm_w4* A) {
-  return static_cast<int64_t>(A->count) * w4_strips(A->M) * w4_units(A->K);
+  return static_cast<int64_t>(A->count) * w4_blocks(A->M) * 8 * w4_units(A->K);
 }
 
 }  // namespace

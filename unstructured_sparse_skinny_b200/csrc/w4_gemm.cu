@@ -2,8 +2,9 @@
 // more tokens than a warp's own fragments serve well.
 //
 // The work is blocks of 128 rows times units of 128 columns; every SM runs one
-// CTA over an equal run of these steps.  Sixteen warps turn codes into 16-bit
-// weights in registers (s * (q - z), rounded once) and store them straight to
+// CTA over an equal run of these steps.  Bulk copies bring codes and
+// activations into shared memory; sixteen warps turn codes into 16-bit weights
+// in registers (s * (q - z), rounded once) and store them straight to
 // tensor memory, where tcgen05.mma takes its A operand from: the weights never
 // pass through shared memory, whose bandwidth the activations need.  The
 // 16x128b store shape places a lane's fragment registers as the packed
@@ -15,7 +16,8 @@
 //
 // A block that one CTA has whole is stored at once.  The sums of one that
 // several CTAs share go to the workspace, and the last of them to arrive adds
-// them in their order.
+// them in their order.  Four warps do this behind the products; at the end of
+// its run the whole CTA joins in, since nothing is left to overlap with.
 #include <atomic>
 #include <type_traits>
 
@@ -27,13 +29,15 @@ namespace {
 
 constexpr int kDequantWarps = 16;          // four groups of four
 constexpr int kEpilogueWarp = 16;          // 16 .. 19
-constexpr int kMmaWarp = 20;               // 21 loads the activations
-constexpr int kThreads = 22 * 32;
+constexpr int kMmaWarp = 20;               // 20, 21
+constexpr int kLoadWarp = 22;              // 22 the activations, 23 the codes
+constexpr int kThreads = 24 * 32;
 constexpr int kBlockRows = 128;
 constexpr int kMaxSlots = 4;               // units between codes and product; slot j is filled by group j alone
-constexpr int kTileBytes = 200 * 1024;     // shared memory for the activations
+constexpr int kMaxRing = 12;               // units of codes in shared memory
+constexpr int kSharedBytes = 224 * 1024;   // for activations and codes
 constexpr uint32_t kUnitTmemCols = 64;     // 128 values of 16 bits
-constexpr uint32_t kAccCols = 256;         // one accumulator, or two of up to 128 columns
+constexpr uint32_t kAccCols = 256;         // accumulators: see Accumulators
 constexpr uint64_t kWaitBudgetNs = 1000000000ull;
 
 struct GemmParams {
@@ -45,7 +49,7 @@ struct GemmParams {
   int64_t ldc;
   bool c_f32;
   int32_t N, n_pad;
-  int32_t slots;
+  int32_t slots, ring;
   int64_t steps;         // blocks * units
   int* status;
 };
@@ -140,17 +144,26 @@ __device__ __forceinline__ __nv_bfloat162 pair_of(uint16_t b, __nv_bfloat16) {
   return __bfloat162bfloat162(__ushort_as_bfloat16(b));
 }
 
-// Codes, scales and zero points of one unit of one strip as a lane holds them.
+// A block's unit in shared memory: codes, scales, zero points of its 8 strips.
+template <int NG>
+struct Shared {
+  static constexpr int kCodes = 8 * kW4UnitBytes, kScales = 8 * 16 * NG * 2, kZeros = 8 * 16 * NG;
+  static constexpr int kBytes = kCodes + kScales + kZeros;
+};
+
+// Codes, scales and zero points of one strip of it as a lane holds them.
 template <typename T, int NG>
 struct Unit {
   uint4 c[2];
   W4Groups<T, NG> g;
 
-  __device__ __forceinline__ void load(const W4Dev& A, int64_t unit, int lane) {
-    const uint4* p = A.codes + unit * 64 + lane;
-    c[0] = ld_stream(p);
-    c[1] = ld_stream(p + 32);
-    g.load(A, unit, lane >> 2);
+  __device__ __forceinline__ void load(const uint8_t* unit, int strip, int lane, bool zeros) {
+    const uint4* p = reinterpret_cast<const uint4*>(unit + strip * kW4UnitBytes) + lane;
+    c[0] = p[0];
+    c[1] = p[32];
+    const int at = (strip * 8 + (lane >> 2)) * (2 * NG);
+    g.load(reinterpret_cast<const uint16_t*>(unit + Shared<NG>::kCodes) + at,
+           zeros ? unit + Shared<NG>::kCodes + Shared<NG>::kScales + at : nullptr);
   }
 
   // Half a unit (64 columns) as 16 registers of 16-bit weights.
@@ -180,18 +193,46 @@ __device__ __forceinline__ uint32_t idesc_of(int n) {
   return umma_idesc_f16_f32(kBlockRows, n) | (type << 7) | (type << 10);
 }
 
-__device__ __forceinline__ void store_out(const GemmParams& p, int64_t n, int64_t m, float v, __half) {
-  if (p.c_f32)
-    static_cast<float*>(p.C)[n * p.ldc + m] = v;
-  else
-    static_cast<__half*>(p.C)[n * p.ldc + m] = __float2half_rn(v);
+template <typename T>
+__device__ __forceinline__ void store_row(const GemmParams& p, int64_t m, int32_t n0, const float (&v)[16]) {
+  // 16 tokens of one row; a warp's lanes hold neighbouring rows
+  const int32_t count = p.N - n0;
+  if (p.c_f32) {
+    float* c = static_cast<float*>(p.C) + n0 * p.ldc + m;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, c += p.ldc)
+      if (j < count) *c = v[j];
+  } else {
+    T* c = static_cast<T*>(p.C) + n0 * p.ldc + m;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, c += p.ldc)
+      if (j < count) *c = from_float<T>(v[j]);
+  }
 }
-__device__ __forceinline__ void store_out(const GemmParams& p, int64_t n, int64_t m, float v, __nv_bfloat16) {
-  if (p.c_f32)
-    static_cast<float*>(p.C)[n * p.ldc + m] = v;
-  else
-    static_cast<__nv_bfloat16*>(p.C)[n * p.ldc + m] = __float2bfloat16_rn(v);
+
+template <typename T>
+__device__ __forceinline__ void store_four(const GemmParams& p, int32_t n, int64_t m, const float4& v) {
+  const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (m + j < p.A.M) {
+      if (p.c_f32)
+        static_cast<float*>(p.C)[n * p.ldc + m + j] = x[j];
+      else
+        static_cast<T*>(p.C)[n * p.ldc + m + j] = from_float<T>(x[j]);
+    }
 }
+
+// Two warps issue products, for every other unit each and into an accumulator
+// of its own, where one could not issue as fast as a unit of few tokens is
+// done (N <= 128); up to 64 tokens there is room for two blocks' accumulators.
+struct Accumulators {
+  int issuers, buffers;
+  uint32_t cols;  // of one
+  __device__ __forceinline__ explicit Accumulators(int32_t n_pad)
+      : issuers(n_pad <= 128 ? 2 : 1), buffers(n_pad <= 64 ? 2 : 1), cols(n_pad <= 64 ? 64 : n_pad <= 128 ? 128 : 256) {}
+  __device__ __forceinline__ uint32_t at(int issuer, int buffer) const { return (buffer * issuers + issuer) * cols; }
+};
 
 // ---------------------------------------------------------------- kernel
 
@@ -220,10 +261,92 @@ __device__ __forceinline__ int64_t run_owner(int64_t steps, int64_t q, int64_t c
   return c;
 }
 
+// The accumulators of a segment to C (a whole block) or to the CTA's slot of
+// the workspace, by `groups` warps per 32 rows, this one the `group`-th.
+template <typename T>
+__device__ __forceinline__ void drain_segment(const GemmParams& p, const Segment& seg, const Accumulators& acc,
+                                              uint32_t tmem, int buffer, int64_t q0, int group, int groups, int quad,
+                                              int lane) {
+  const int row = quad * 32 + lane;
+  const int64_t m = seg.block * kBlockRows + row;
+  const uint32_t from = tmem + acc.at(0, buffer) + (static_cast<uint32_t>(quad * 32) << 16);
+  const int first = static_cast<int>((seg.from - q0) & 1);
+  // with two issuers: a segment of one unit has one sum, in its issuer's accumulator
+  const bool both = acc.issuers == 2 && seg.to - seg.from > 1;
+  const uint32_t one = acc.issuers == 2 && !both ? first * acc.cols : 0;
+  float* part = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (seg.from > q0)) * p.n_pad * kBlockRows + row;
+  for (int32_t n0 = group * 16; n0 < p.n_pad; n0 += groups * 16) {
+    uint32_t a[16], b[16];
+    tmem_load_16(from + one + n0, a);
+    if (both) tmem_load_16(from + acc.cols + n0, b);
+    tmem_load_wait();
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      v[j] = both ? __uint_as_float(a[j]) + __uint_as_float(b[j]) : __uint_as_float(a[j]);
+    if (!seg.whole) {
+      float* o = part + n0 * kBlockRows;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j * kBlockRows] = v[j];
+    } else if (m < p.A.M) {
+      store_row<T>(p, m, n0, v);
+    }
+  }
+}
+
+// The CTAs that share a block.
+struct Sharers {
+  int64_t first, last;
+  int64_t first_slot;  // the others hold the block first in their run
+  __device__ __forceinline__ Sharers(const GemmParams& p, int64_t block) {
+    const int64_t from = block * p.A.units;
+    first = run_owner(p.steps, from, gridDim.x);
+    last = run_owner(p.steps, from + p.A.units - 1, gridDim.x);
+    first_slot = first * 2 + (run_begin(p.steps, first, gridDim.x) < from);
+  }
+};
+
+// All sums of a shared block, in the order of its CTAs, by `threads` threads.
+template <typename T>
+__device__ __forceinline__ void join_block(const GemmParams& p, int64_t block, const Sharers& who, int tid,
+                                           int threads) {
+  constexpr int kBatch = 4;  // loads in flight a thread and CTA
+  const int32_t total = p.N * (kBlockRows / 4);
+  const float4* base = reinterpret_cast<const float4*>(p.partials);
+  const int64_t slot = static_cast<int64_t>(p.n_pad) * (kBlockRows / 4);
+  for (int32_t i0 = tid; i0 < total; i0 += threads * kBatch) {
+    float4 sum[kBatch] = {};
+    for (int64_t c = who.first; c <= who.last; c += 2) {
+      const float4* s0 = base + (c == who.first ? who.first_slot : c * 2) * slot;
+      const float4* s1 = base + (c + 1) * 2 * slot;
+      const bool second = c < who.last;
+      float4 v0[kBatch], v1[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int32_t i = i0 + threads * j;
+        v0[j] = i < total ? __ldcg(s0 + i) : make_float4(0, 0, 0, 0);
+        v1[j] = second && i < total ? __ldcg(s1 + i) : make_float4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        sum[j].x = sum[j].x + v0[j].x + v1[j].x;
+        sum[j].y = sum[j].y + v0[j].y + v1[j].y;
+        sum[j].z = sum[j].z + v0[j].z + v1[j].z;
+        sum[j].w = sum[j].w + v0[j].w + v1[j].w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int32_t i = i0 + threads * j;
+      if (i < total) store_four<T>(p, i / (kBlockRows / 4), block * kBlockRows + (i % (kBlockRows / 4)) * 4, sum[j]);
+    }
+  }
+}
+
 template <typename T, int NG>
 __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t full[kMaxSlots], used[kMaxSlots], acc_full[2], acc_empty[2];
+  __shared__ uint64_t codes_full[kMaxRing], codes_used[kMaxRing], full[kMaxSlots], used[kMaxSlots], acc_full[2], acc_empty[2], mma_done[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word, last_word;
   volatile int* abort_flag = &abort_word;
@@ -231,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   const int32_t units = p.A.units;
   const int64_t q0 = run_begin(p.steps, blockIdx.x, gridDim.x), q1 = run_begin(p.steps, blockIdx.x + 1, gridDim.x);
   const uint32_t stage_bytes = static_cast<uint32_t>(p.n_pad) * 256;
-  const int accs = p.n_pad <= 128 ? 2 : 1;
+  const Accumulators acc(p.n_pad);
   uint8_t* tiles = smem + ((1024 - (smem_u32(smem) & 1023)) & 1023);
+  uint8_t* codes = tiles + p.slots * stage_bytes;
 
   if (threadIdx.x == 0) {
     abort_word = 0;
@@ -240,9 +364,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
       mbar_init(&full[i], 5);  // four warps' weights and the copy of the activations
       mbar_init(&used[i], 1);
     }
+    for (int i = 0; i < kMaxRing; ++i) {
+      mbar_init(&codes_full[i], 1);
+      mbar_init(&codes_used[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_full[i], acc.issuers);
       mbar_init(&acc_empty[i], 4);
+      mbar_init(&mma_done[i], 1);
     }
     fence_barrier_init();
   }
@@ -257,28 +386,20 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
 
   if (warp < kDequantWarps) {
     // ---- codes -> tensor memory: 32 rows of the units of one slot.  (A slot that groups took in turns could
-    // be two phases ahead of a group's wait, which parity does not tell from none.)
+    // be two phases ahead of a group's wait, which parity does not tell from none; the ring of codes is a
+    // multiple of the slots for the same reason.)
     const int quad = warp & 3, group = warp >> 2;
     const uint32_t dst = tmem + kAccCols + group * kUnitTmemCols + (static_cast<uint32_t>(quad * 32) << 16);
     const int64_t end = group < p.slots ? q1 : q0;  // no work for a group without a slot
-    int64_t block = (q0 + group) / units;
-    int32_t u = static_cast<int32_t>(q0 + group - block * units);
-    const auto load = [&](Unit<T, NG> (&x)[2]) {
-      const int64_t strip = block * 8 + quad * 2;
-      x[0].load(p.A, min64(strip, p.A.strips - 1) * units + u, lane);
-      x[1].load(p.A, min64(strip + 1, p.A.strips - 1) * units + u, lane);
-      u += p.slots;
-      while (u >= units) {
-        u -= units;
-        ++block;
-      }
-    };
-    Unit<T, NG> now[2];
-    if (q0 + group < end) load(now);
-    uint32_t phase = 1;
+    const bool zeros = p.A.zeros != nullptr;
+    uint32_t phase = 1, ring_phase = 0;
+    int ring = group;
     for (int64_t q = q0 + group; q < end; q += p.slots, phase ^= 1) {
-      Unit<T, NG> next[2];
-      if (q + p.slots < end) load(next);
+      if (!mbar_wait(&codes_full[ring], ring_phase, abort_flag, kWaitBudgetNs, p.status)) break;
+      __syncwarp();
+      Unit<T, NG> strip[2];
+      strip[0].load(codes + ring * Shared<NG>::kBytes, quad * 2, lane, zeros);
+      strip[1].load(codes + ring * Shared<NG>::kBytes, quad * 2 + 1, lane, zeros);
       if (!mbar_wait(&used[group], phase, abort_flag, kWaitBudgetNs, p.status)) break;
       __syncwarp();
       tc_fence_after_sync();
@@ -287,186 +408,181 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t r[16];
-          now[j].weights(half, r);
+          strip[j].weights(half, r);
           tmem_store_16x32(dst + half * (kUnitTmemCols / 2) + (static_cast<uint32_t>(16 * j) << 16), r);
         }
+      if (lane == 0) mbar_arrive(&codes_used[ring]);  // read into registers by all lanes: see the __syncwarp above
       tmem_store_wait();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[group]);
-      now[0] = next[0];
-      now[1] = next[1];
+      ring += p.slots;
+      if (ring >= p.ring) {
+        ring -= p.ring;
+        ring_phase ^= 1;
+      }
     }
   } else if (warp < kMmaWarp) {
-    // ---- accumulators -> C or the workspace
+    // ---- all blocks of the run but the last: accumulators -> C or the workspace, behind the products
     griddep_wait();
-    const int quad = warp & 3;
-    const int row = quad * 32 + lane;
-    int count = 0;
-    for (int64_t q = q0; q < q1; ++count) {
+    int buffer = 0;
+    uint32_t phase = 0;
+    for (int64_t q = q0;;) {
       const Segment seg = segment_at(q, q1, units);
+      if (seg.to == q1) break;
       q = seg.to;
-      const int ab = count % accs;
       // a wait that runs out leaves wrong values and an error, not a warp missing at the barriers below
-      mbar_wait(&acc_full[ab], static_cast<uint32_t>((count / accs) & 1), abort_flag, kWaitBudgetNs, p.status);
+      mbar_wait(&acc_full[buffer], phase, abort_flag, kWaitBudgetNs, p.status);
       __syncwarp();
       tc_fence_after_sync();
-      const int64_t m = seg.block * kBlockRows + row;
-      const int64_t slot_size = static_cast<int64_t>(p.n_pad) * kBlockRows;
-      float* part = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (seg.from > q0)) * slot_size;
-      for (int32_t n0 = 0; n0 < p.n_pad; n0 += 16) {
-        uint32_t r[16];
-        tmem_load_16(tmem + ab * 128 + (static_cast<uint32_t>(quad * 32) << 16) + n0, r);
-        tmem_load_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (!seg.whole)
-            part[(n0 + j) * kBlockRows + row] = __uint_as_float(r[j]);
-          else if (n0 + j < p.N && m < p.A.M)
-            store_out(p, n0 + j, m, __uint_as_float(r[j]), T());
-        }
-      }
+      drain_segment<T>(p, seg, acc, tmem, buffer, q0, 0, 1, warp & 3, lane);
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      if (lane == 0) mbar_arrive(&acc_empty[buffer]);
+      if (++buffer == acc.buffers) {
+        buffer = 0;
+        phase ^= 1;
+      }
       if (seg.whole) continue;
-      // the last of the block's CTAs adds all their sums, in order
-      const int64_t first = run_owner(p.steps, seg.block * units, gridDim.x);
-      const int64_t last = run_owner(p.steps, (seg.block + 1) * units - 1, gridDim.x);
+      const Sharers who(p, seg.block);
       __threadfence();
       named_barrier(1, 128);
-      if (threadIdx.x == kEpilogueWarp * 32)
-        last_word = atomicAdd(&p.arrived[seg.block], 1) == static_cast<int32_t>(last - first);
+      if (warp == kEpilogueWarp && lane == 0)
+        last_word = atomicAdd(&p.arrived[seg.block], 1) == static_cast<int32_t>(who.last - who.first);
       named_barrier(1, 128);
       if (!last_word) continue;
       __threadfence();
-      const int tid = threadIdx.x - kEpilogueWarp * 32;
-      // the block is the last of its first contributor's run, unless that run begins with it, and the first
-      // of the others' runs
-      const int64_t first_slot = first * 2 + (run_begin(p.steps, first, gridDim.x) < seg.block * units);
-      const float4* base = reinterpret_cast<const float4*>(p.partials);
-      const int64_t step = slot_size / 4;
-      constexpr int kBatch = 8;  // loads in flight a thread
-      for (int32_t i0 = tid; i0 < p.N * (kBlockRows / 4); i0 += 128 * kBatch) {
-        float4 sum[kBatch] = {};
-        for (int64_t c = first; c <= last; ++c) {
-          const float4* src = base + (c == first ? first_slot : c * 2) * step;
-          float4 v[kBatch];
+      join_block<T>(p, seg.block, who, threadIdx.x - kEpilogueWarp * 32, 128);
+    }
+  } else if (warp < kLoadWarp) {
+    // ---- products: the warp walks the units as one and an elected lane issues (a loop of one lane alone
+    // cannot keep the descriptors in uniform registers and took twice as long a unit)
+    const int me = warp - kMmaWarp;
+    if (me < acc.issuers) {
+      const uint32_t idesc = idesc_of<T>(p.n_pad);
+      const uint64_t desc0 = smem_desc_k_sw128(smem_u32(tiles));
+      const uint32_t half = stage_bytes / 2 / 16;  // descriptor addresses count 16 bytes
+      int32_t left = static_cast<int32_t>(min64(q1 - q0, units - q0 % units));  // steps of the current segment
+      int64_t rest = q1 - q0;
+      int slot = me, buffer = 0, skip = me;  // steps until the next one of this warp
+      uint32_t phase = 0, acc_phase = 1;
+      bool dead = false;
+      while (rest > 0 && !dead) {
+        if (!mbar_wait(&acc_empty[buffer], acc_phase, abort_flag, kWaitBudgetNs, p.status)) break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + acc.at(me, buffer);
+        uint32_t accumulate = 0;
+        rest -= left;
+        int32_t at = skip;
+        for (; at < left; at += acc.issuers) {
+          if (!mbar_wait(&full[slot], phase, abort_flag, kWaitBudgetNs, p.status)) {
+            dead = true;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t desc = desc0 + static_cast<uint32_t>(slot) * (2 * half);
+          const uint32_t a = tmem + kAccCols + slot * kUnitTmemCols;
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            v[j] = i0 + 128 * j < p.N * (kBlockRows / 4) ? __ldcg(src + i0 + 128 * j) : make_float4(0, 0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            sum[j].x += v[j].x;
-            sum[j].y += v[j].y;
-            sum[j].z += v[j].z;
-            sum[j].w += v[j].w;
+            for (int s = 0; s < 8; ++s)
+              umma_f16_ts(d, a + s * 8, desc + (s >> 2) * half + (s & 3) * 2, idesc, s == 0 ? accumulate : 1u);
+            umma_commit(&used[slot]);
+          }
+          __syncwarp();
+          accumulate = 1;
+          slot += acc.issuers;
+          if (slot >= p.slots) {
+            slot -= p.slots;
+            phase ^= 1;
           }
         }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int32_t i = i0 + 128 * j;
-          if (i >= p.N * (kBlockRows / 4)) break;
-          const int32_t n = i / (kBlockRows / 4);
-          const int64_t r = seg.block * kBlockRows + (i % (kBlockRows / 4)) * 4;
-          const float v[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (r + k < p.A.M) store_out(p, n, r + k, v[k], T());
-        }
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- all products: the warp walks the units as one, an elected lane issues.  (With only that lane in
-    // the loop the descriptors cannot stay in uniform registers: 1275 instead of %s cycles a unit of 64 tokens.)
-    const uint32_t idesc = idesc_of<T>(p.n_pad);
-    const uint64_t desc0 = smem_desc_k_sw128(smem_u32(tiles));
-    const uint32_t half = stage_bytes / 2 / 16;  // descriptor addresses count 16 bytes
-    int32_t left = static_cast<int32_t>(min64(q1 - q0, units - q0 % units));  // steps of the current segment
-    int64_t rest = q1 - q0;
-    int slot = 0, ab = 0, done_ab = 0;
-    uint32_t phase = 0, acc_phase = 1, done_phase = 0;
-    bool dead = false, any = false;
-    while (rest > 0 && !dead) {
-      if (!mbar_wait(&acc_empty[ab], acc_phase, abort_flag, kWaitBudgetNs, p.status)) break;
-      tc_fence_after_sync();
-      const uint32_t acc = tmem + ab * 128;
-      uint32_t accumulate = 0;
-      rest -= left;
-      for (; left > 0; --left) {
-        if (!mbar_wait(&full[slot], phase, abort_flag, kWaitBudgetNs, p.status)) {
-          dead = true;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint64_t desc = desc0 + static_cast<uint32_t>(slot) * (2 * half);
-        const uint32_t a = tmem + kAccCols + slot * kUnitTmemCols;
-        if (elect_one()) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            umma_f16_ts(acc, a + s * 8, desc + (s >> 2) * half + (s & 3) * 2, idesc, s == 0 ? accumulate : 1u);
-          umma_commit(&used[slot]);
-          if (left == 1) umma_commit(&acc_full[ab]);
-        }
+        if (dead) break;
+        skip = at - left;
+        if (elect_one()) umma_commit(&acc_full[buffer]);
         __syncwarp();
-        accumulate = 1;
-        if (++slot == p.slots) {
+        if (++buffer == acc.buffers) {
+          buffer = 0;
+          acc_phase ^= 1;
+        }
+        left = static_cast<int32_t>(min64(rest, units));
+      }
+      if (elect_one()) umma_commit(&mma_done[me]);
+    }
+  } else {
+    // ---- bulk copies: codes, which nothing holds back, run ahead of the activations
+    if (lane == 0) {
+      const bool of_codes = warp > kLoadWarp;
+      if (!of_codes) griddep_wait();
+      const int slots = of_codes ? p.ring : p.slots;
+      uint64_t* filled = of_codes ? codes_full : full;
+      uint64_t* freed = of_codes ? codes_used : used;
+      const uint32_t zero_bytes = p.A.zeros ? Shared<NG>::kZeros : 0;
+      const uint32_t bytes = of_codes ? Shared<NG>::kCodes + Shared<NG>::kScales + zero_bytes : stage_bytes;
+      int32_t u = static_cast<int32_t>(q0 % units);
+      int slot = 0, issued = 0;
+      uint32_t phase = 1;
+      for (int64_t q = q0; q < q1; ++q) {
+        if (!mbar_wait(&freed[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
+        mbar_arrive_expect_tx(&filled[slot], bytes);
+        if (of_codes) {
+          // a block's units are consecutive: step q is the matrix's q-th
+          uint8_t* to = codes + slot * Shared<NG>::kBytes;
+          bulk_load(to, reinterpret_cast<const uint8_t*>(p.A.codes) + q * Shared<NG>::kCodes, Shared<NG>::kCodes,
+                    &filled[slot]);
+          bulk_load(to + Shared<NG>::kCodes, reinterpret_cast<const uint8_t*>(p.A.scales) + q * Shared<NG>::kScales,
+                    Shared<NG>::kScales, &filled[slot]);
+          if (zero_bytes)
+            bulk_load(to + Shared<NG>::kCodes + Shared<NG>::kScales, p.A.zeros + q * Shared<NG>::kZeros, zero_bytes,
+                      &filled[slot]);
+        } else {
+          bulk_load(tiles + slot * stage_bytes, p.image + static_cast<int64_t>(u) * stage_bytes, stage_bytes,
+                    &filled[slot]);
+          if (++u == units) u = 0;
+        }
+        if (issued < slots) ++issued;
+        if (++slot == slots) {
           slot = 0;
           phase ^= 1;
         }
       }
-      if (dead) break;
-      any = true;
-      done_ab = ab;
-      done_phase = acc_phase ^ 1;
-      if (++ab == accs) {
-        ab = 0;
-        acc_phase ^= 1;
+      // Copies in flight land before the CTA leaves: a phase ends with its copy, and for the activations with
+      // the unit's weights; when another role has given up only a bounded wait is left to do.
+      for (; issued > 0; --issued) {
+        if (--slot < 0) {
+          slot = slots - 1;
+          phase ^= 1;
+        }
+        mbar_wait_drain(&filled[slot], phase ^ 1, kWaitBudgetNs, p.status);
       }
-      left = static_cast<int32_t>(min64(rest, units));
-    }
-    // everything issued has completed before tensor memory is given back
-    if (dead) {
-      if (elect_one()) umma_commit(&acc_full[ab]);
-      __syncwarp();
-      mbar_wait_drain(&acc_full[ab], acc_phase ^ 1, kWaitBudgetNs, p.status);
-    } else if (any) {
-      mbar_wait_drain(&acc_full[done_ab], done_phase, kWaitBudgetNs, p.status);
-    }
-    __syncwarp();
-  } else if (lane == 0) {
-    // ---- activations: one bulk copy per unit
-    griddep_wait();
-    int32_t u = static_cast<int32_t>(q0 % units);
-    int slot = 0, issued = 0;
-    uint32_t phase = 1;
-    for (int64_t q = q0; q < q1; ++q) {
-      if (!mbar_wait(&used[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
-      mbar_arrive_expect_tx(&full[slot], stage_bytes);
-      bulk_load(tiles + slot * stage_bytes, p.image + static_cast<int64_t>(u) * stage_bytes, stage_bytes, &full[slot]);
-      if (++u == units) u = 0;
-      if (issued < p.slots) ++issued;
-      if (++slot == p.slots) {
-        slot = 0;
-        phase ^= 1;
-      }
-    }
-    // Copies in flight land before the CTA leaves: a unit's phase ends with its copy and its weights, and
-    // when another role has given up only a bounded wait is left to do.
-    for (; issued > 0; --issued) {
-      if (--slot < 0) {
-        slot = p.slots - 1;
-        phase ^= 1;
-      }
-      mbar_wait_drain(&full[slot], phase ^ 1, kWaitBudgetNs, p.status);
     }
   }
+
+  // ---- the run's last block, by all warps.  (They wait for the end of all products: a phase of acc_full
+  // could still be two ahead of a warp that comes here early, which parity does not tell from none.)
+  __syncwarp();
+  const int64_t last_block = (q1 - 1) / units, before = last_block - q0 / units;
+  const Segment seg = segment_at(max64(q0, last_block * units), q1, units);
+  const int buffer = static_cast<int>(before % acc.buffers);
+  griddep_wait();
+  for (int i = 0; i < acc.issuers; ++i) mbar_wait_drain(&mma_done[i], 0, kWaitBudgetNs, p.status);
+  __syncwarp();
+  tc_fence_after_sync();
+  if (warp < kMmaWarp) drain_segment<T>(p, seg, acc, tmem, buffer, q0, warp >> 2, kMmaWarp / 4, warp & 3, lane);
   tc_fence_before_sync();
+  if (!seg.whole) __threadfence();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
+  if (seg.whole) return;
+  const Sharers who(p, seg.block);
+  if (threadIdx.x == 0)
+    last_word = atomicAdd(&p.arrived[seg.block], 1) == static_cast<int32_t>(who.last - who.first);
+  __syncthreads();
+  if (!last_word) return;
+  __threadfence();
+  join_block<T>(p, seg.block, who, threadIdx.x, kThreads);
 }
 
 int32_t pad_n(int32_t N) { return (N + 15) / 16 * 16; }
@@ -494,21 +610,27 @@ GemmWorkspace layout(int32_t M, int32_t K, int32_t N) {
 }
 
 template <typename T, int NG>
-cudaError_t launch_as(const GemmParams& p, int64_t ctas, cudaStream_t s) {
+cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
+  // four units between codes and product where they fit beside as many of codes; the more codes the better:
+  // an SM's share of HBM needs some 35 KB in flight
+  const int32_t tile = p.n_pad * 256;
+  p.slots = p.n_pad <= 128 ? 4 : 3;
+  p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * tile) / Shared<NG>::kBytes)) / p.slots *
+           p.slots;
   auto kernel = w4_gemm_kernel<T, NG>;
   static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(allowed.load() >> (dev & 63) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytes + 1024);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes + 1024);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(uint64_t(1) << (dev & 63));
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.slots) * p.n_pad * 256 + 1024;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.slots) * p.n_pad * 256 + p.ring * Shared<NG>::kBytes + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -536,7 +658,6 @@ cudaError_t launch_w4_gemm(const flashspmm_w4* in, const void* B, int64_t ldb, v
   p.c_f32 = c_f32;
   p.N = N;
   p.n_pad = pad_n(N);
-  p.slots = static_cast<int32_t>(min64(kMaxSlots, kTileBytes / (p.n_pad * 256)));
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInitializationError;
   const int64_t blocks = (static_cast<int64_t>(p.A.M) + kBlockRows - 1) / kBlockRows;

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kWarps * 32) w4_matmul_kernel(W4Dev A, const u
     W4Groups<T, NG> grp[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t unit = static_cast<int64_t>(min(strip0 + r, A.strips - 1)) * A.units + u;
+      const int64_t unit = A.unit(0, min(strip0 + r, A.strips - 1), u);
       c[r][0] = ld_stream(A.codes + unit * 64 + lane);
       c[r][1] = ld_stream(A.codes + unit * 64 + 32 + lane);
       grp[r].load(A, unit, g);

@@ -36,8 +36,8 @@ class _W4View(ctypes.Structure):
 @dataclass(frozen=True, eq=False)
 class W4:
     """A 4-bit matrix [M, K], or a stack [count, M, K], in device memory."""
-    codes: torch.Tensor          # uint8 [count, strips, units, 1024]
-    scales: torch.Tensor         # float16 or bfloat16 [count, strips, units, 8, 128 // group, 2]
+    codes: torch.Tensor          # uint8 [count, blocks, units, 8, 1024]: blocks of 128 rows, units of 128 columns
+    scales: torch.Tensor         # float16 or bfloat16 [count, blocks, units, 8, 8, 128 // group, 2]
     zeros: torch.Tensor | None   # uint8, the scales' shape; None: every zero point is 8
     M: int
     K: int
@@ -144,9 +144,9 @@ def _empty(shape, dtype: torch.dtype, group: int, symmetric: bool, device: torch
     if lib.flashspmm_w4_sizes(M, K, count, group, None, None, None) != 0:
         raise ValueError(f"4-bit weights need group 32, 64 or 128 and at least one matrix, got group {group}, "
                          f"shape {tuple(shape)}")
-    strips, units = -(-M // 16), -(-K // 128)
-    per = (count, strips, units, 8, 128 // group, 2)
-    return W4(torch.empty((count, strips, units, 1024), dtype=torch.uint8, device=device),
+    blocks, units = -(-M // 128), -(-K // 128)
+    per = (count, blocks, units, 8, 8, 128 // group, 2)
+    return W4(torch.empty((count, blocks, units, 8, 1024), dtype=torch.uint8, device=device),
               torch.empty(per, dtype=dtype, device=device),
               None if symmetric else torch.empty(per, dtype=torch.uint8, device=device), M, K, group, len(shape) == 3)
 

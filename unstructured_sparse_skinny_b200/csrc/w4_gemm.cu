@@ -27,13 +27,13 @@
 namespace flashspmm {
 namespace {
 
-constexpr int kDequantWarps = 16;          // four groups of four
+constexpr int kDequantWarps = 16;
 constexpr int kEpilogueWarp = 16;          // 16 .. 19
 constexpr int kMmaWarp = 20;               // 20, 21
 constexpr int kLoadWarp = 22;              // 22 the activations, 23 the codes
 constexpr int kThreads = 24 * 32;
 constexpr int kBlockRows = 128;
-constexpr int kMaxSlots = 4;               // units between codes and product; slot j is filled by group j alone
+constexpr int kMaxSlots = 4;               // units between codes and product
 constexpr int kMaxRing = 12;               // units of codes in shared memory
 constexpr int kSharedBytes = 224 * 1024;   // for activations and codes
 constexpr uint32_t kUnitTmemCols = 64;     // 128 values of 16 bits
@@ -98,13 +98,19 @@ __device__ __forceinline__ void bulk_load(void* smem, const void* src, uint32_t 
 }
 
 // 16 TMEM lanes x 32 columns: register 2 i is row g, 2 i + 1 row g + 8 of column 4 i + t.
-__device__ __forceinline__ void tmem_store_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// 16 TMEM lanes x 16 columns, likewise.
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -121,27 +127,15 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
 
 // ---------------------------------------------------------------- codes to 16-bit weights
 
-__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 s) {
-  union {
-    uint32_t u;
-    __half2 h;
-  } x;
-  x.u = a;
-  x.h = __hmul2(x.h, s);
-  return x.u;
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s, __half) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(s));
+  return r;
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, __nv_bfloat162 s) {
-  union {
-    uint32_t u;
-    __nv_bfloat162 h;
-  } x;
-  x.u = a;
-  x.h = __hmul2(x.h, s);
-  return x.u;
-}
-__device__ __forceinline__ __half2 pair_of(uint16_t b, __half) { return __half2half2(__ushort_as_half(b)); }
-__device__ __forceinline__ __nv_bfloat162 pair_of(uint16_t b, __nv_bfloat16) {
-  return __bfloat162bfloat162(__ushort_as_bfloat16(b));
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s, __nv_bfloat16) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(s));
+  return r;
 }
 
 // A block's unit in shared memory: codes, scales, zero points of its 8 strips.
@@ -151,37 +145,54 @@ struct Shared {
   static constexpr int kBytes = kCodes + kScales + kZeros;
 };
 
-// Codes, scales and zero points of one strip of it as a lane holds them.
-template <typename T, int NG>
-struct Unit {
-  uint4 c[2];
-  W4Groups<T, NG> g;
+// The P-th part (128 / P columns) of one strip of it as a lane holds it: codes, then 16-bit weights.
+template <typename T, int NG, int P>
+struct Part {
+  static constexpr int kWords = 8 / P;                   // of 8 codes
+  static constexpr int kGroups = NG > P ? NG / P : 1;    // scales that touch the part
+  uint32_t w[kWords];
+  uint32_t s[kGroups], z[kGroups];                       // {row g, row g + 8}
 
-  __device__ __forceinline__ void load(const uint8_t* unit, int strip, int lane, bool zeros) {
-    const uint4* p = reinterpret_cast<const uint4*>(unit + strip * kW4UnitBytes) + lane;
-    c[0] = p[0];
-    c[1] = p[32];
-    const int at = (strip * 8 + (lane >> 2)) * (2 * NG);
-    g.load(reinterpret_cast<const uint16_t*>(unit + Shared<NG>::kCodes) + at,
-           zeros ? unit + Shared<NG>::kCodes + Shared<NG>::kScales + at : nullptr);
+  __device__ __forceinline__ void load(const uint8_t* unit, int strip, int part, int lane, bool zeros) {
+    if (P == 2) {
+      const uint4 v = *reinterpret_cast<const uint4*>(unit + strip * kW4UnitBytes + part * 512 + lane * 16);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2 % kWords] = v.z;
+      w[3 % kWords] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(unit + strip * kW4UnitBytes + (part >> 1) * 512 + lane * 16 +
+                                                      (part & 1) * 8);
+      w[0] = v.x;
+      w[1] = v.y;
+    }
+    const int at = (strip * 8 + (lane >> 2)) * (2 * NG) + 2 * (part * NG / P);
+    const uint8_t* scales = unit + Shared<NG>::kCodes + at * 2;
+    const uint8_t* points = unit + Shared<NG>::kCodes + Shared<NG>::kScales + at;
+    if (kGroups == 1) {
+      s[0] = *reinterpret_cast<const uint32_t*>(scales);
+      z[0] = zeros ? *reinterpret_cast<const uint16_t*>(points) : 0x0808u;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(scales);
+      s[0] = v.x;
+      s[kGroups - 1] = v.y;
+      const uint32_t q = zeros ? *reinterpret_cast<const uint32_t*>(points) : 0x08080808u;
+      z[0] = q & 0xFFFF;
+      z[kGroups - 1] = q >> 16;
+    }
   }
 
-  // Half a unit (64 columns) as 16 registers of 16-bit weights.
-  __device__ __forceinline__ void weights(int half, uint32_t (&r)[16]) const {
+  __device__ __forceinline__ void weights(uint32_t (&r)[4 * kWords]) const {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int gi = (2 * half + b) * NG / 4;
-      const W4Zero<T> zero = g.zero(gi);
-      const auto s0 = pair_of(static_cast<uint16_t>(g.s[gi] & 0xFFFF), T());
-      const auto s1 = pair_of(static_cast<uint16_t>(g.s[gi] >> 16), T());
+    for (int gi = 0; gi < kGroups; ++gi) {
+      const W4Zero<T> zero(static_cast<int>(z[gi] & 0xFF), static_cast<int>(z[gi] >> 8));
+      const uint32_t s0 = __byte_perm(s[gi], 0, 0x1010), s1 = __byte_perm(s[gi], 0, 0x3232);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int i = gi * kWords / kGroups; i < (gi + 1) * kWords / kGroups; ++i) {
         uint32_t a[4];
-        w4_fragment(b == 0 ? (s == 0 ? c[half].x : c[half].y) : (s == 0 ? c[half].z : c[half].w), zero, a);
-        r[8 * b + 4 * s + 0] = mul2(a[0], s0);
-        r[8 * b + 4 * s + 1] = mul2(a[1], s1);
-        r[8 * b + 4 * s + 2] = mul2(a[2], s0);
-        r[8 * b + 4 * s + 3] = mul2(a[3], s1);
+        w4_fragment(w[i], zero, a);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[4 * i + j] = mul2(a[j], j & 1 ? s1 : s0, T());
       }
     }
   }
@@ -343,7 +354,8 @@ __device__ __forceinline__ void join_block(const GemmParams& p, int64_t block, c
   }
 }
 
-template <typename T, int NG>
+// P: warps share the columns of 32 rows of a unit P ways, so 4 / P groups of 4 P warps have units in turn.
+template <typename T, int NG, int P>
 __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t codes_full[kMaxRing], codes_used[kMaxRing], full[kMaxSlots], used[kMaxSlots], acc_full[2], acc_empty[2], mma_done[2];
@@ -361,12 +373,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   if (threadIdx.x == 0) {
     abort_word = 0;
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(&full[i], 5);  // four warps' weights and the copy of the activations
+      mbar_init(&full[i], 4 * P + 1);  // the warps' weights and the copy of the activations
       mbar_init(&used[i], 1);
     }
     for (int i = 0; i < kMaxRing; ++i) {
       mbar_init(&codes_full[i], 1);
-      mbar_init(&codes_used[i], 4);
+      mbar_init(&codes_used[i], 4 * P);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], acc.issuers);
@@ -385,41 +397,44 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   const uint32_t tmem = tmem_slot;
 
   if (warp < kDequantWarps) {
-    // ---- codes -> tensor memory: 32 rows of the units of one slot.  (A slot that groups took in turns could
-    // be two phases ahead of a group's wait, which parity does not tell from none; the ring of codes is a
-    // multiple of the slots for the same reason.)
-    const int quad = warp & 3, group = warp >> 2;
-    const uint32_t dst = tmem + kAccCols + group * kUnitTmemCols + (static_cast<uint32_t>(quad * 32) << 16);
-    const int64_t end = group < p.slots ? q1 : q0;  // no work for a group without a slot
+    // ---- codes -> tensor memory.  A slot, and a place of the ring of codes, belongs to one group: taken in
+    // turns it could be two phases away from a group's wait, which parity does not tell from none.
+    constexpr int kGroups = 4 / P;
+    const int quad = warp & 3, part = (warp >> 2) % P, group = (warp >> 2) / P;
+    const uint32_t dst =
+        tmem + kAccCols + part * (kUnitTmemCols / P) + (static_cast<uint32_t>(quad * 32) << 16);
     const bool zeros = p.A.zeros != nullptr;
     uint32_t phase = 1, ring_phase = 0;
-    int ring = group;
-    for (int64_t q = q0 + group; q < end; q += p.slots, phase ^= 1) {
+    int ring = group, slot = group;
+    for (int64_t q = q0 + group; q < q1; q += kGroups) {
       if (!mbar_wait(&codes_full[ring], ring_phase, abort_flag, kWaitBudgetNs, p.status)) break;
       __syncwarp();
-      Unit<T, NG> strip[2];
-      strip[0].load(codes + ring * Shared<NG>::kBytes, quad * 2, lane, zeros);
-      strip[1].load(codes + ring * Shared<NG>::kBytes, quad * 2 + 1, lane, zeros);
-      if (!mbar_wait(&used[group], phase, abort_flag, kWaitBudgetNs, p.status)) break;
+      uint32_t r[2][32 / P];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        Part<T, NG, P> strip;
+        strip.load(codes + ring * Shared<NG>::kBytes, quad * 2 + j, part, lane, zeros);
+        strip.weights(r[j]);
+      }
+      if (!mbar_wait(&used[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
       __syncwarp();
       tc_fence_after_sync();
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t r[16];
-          strip[j].weights(half, r);
-          tmem_store_16x32(dst + half * (kUnitTmemCols / 2) + (static_cast<uint32_t>(16 * j) << 16), r);
-        }
-      if (lane == 0) mbar_arrive(&codes_used[ring]);  // read into registers by all lanes: see the __syncwarp above
+      tmem_store(dst + slot * kUnitTmemCols, r[0]);
+      tmem_store(dst + slot * kUnitTmemCols + (16u << 16), r[1]);
+      if (lane == 0) mbar_arrive(&codes_used[ring]);  // all lanes have their weights: the stores are the warp's
       tmem_store_wait();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[group]);
-      ring += p.slots;
+      if (lane == 0) mbar_arrive(&full[slot]);
+      ring += kGroups;
       if (ring >= p.ring) {
         ring -= p.ring;
         ring_phase ^= 1;
+      }
+      slot += kGroups;
+      if (slot >= p.slots) {
+        slot -= p.slots;
+        phase ^= 1;
       }
     }
   } else if (warp < kMmaWarp) {
@@ -509,51 +524,64 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
       if (elect_one()) umma_commit(&mma_done[me]);
     }
   } else {
-    // ---- bulk copies: codes, which nothing holds back, run ahead of the activations
-    if (lane == 0) {
-      const bool of_codes = warp > kLoadWarp;
-      if (!of_codes) griddep_wait();
-      const int slots = of_codes ? p.ring : p.slots;
-      uint64_t* filled = of_codes ? codes_full : full;
-      uint64_t* freed = of_codes ? codes_used : used;
-      const uint32_t zero_bytes = p.A.zeros ? Shared<NG>::kZeros : 0;
-      const uint32_t bytes = of_codes ? Shared<NG>::kCodes + Shared<NG>::kScales + zero_bytes : stage_bytes;
-      int32_t u = static_cast<int32_t>(q0 % units);
-      int slot = 0, issued = 0;
-      uint32_t phase = 1;
-      for (int64_t q = q0; q < q1; ++q) {
-        if (!mbar_wait(&freed[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
+    // ---- bulk copies (a warp walks the units, an elected lane issues): the activations of a unit, and by
+    // another warp, which nothing but the ring holds back, its codes
+    const bool of_codes = warp > kLoadWarp;
+    if (!of_codes) griddep_wait();
+    const int slots = of_codes ? p.ring : p.slots;
+    uint64_t* filled = of_codes ? codes_full : full;
+    uint64_t* freed = of_codes ? codes_used : used;
+    const uint32_t zero_bytes = p.A.zeros ? Shared<NG>::kZeros : 0;
+    const uint32_t bytes = of_codes ? Shared<NG>::kCodes + Shared<NG>::kScales + zero_bytes : stage_bytes;
+    // a block's units are consecutive: step q is the matrix's q-th
+    const uint8_t* from = of_codes ? reinterpret_cast<const uint8_t*>(p.A.codes) + q0 * Shared<NG>::kCodes : p.image;
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.A.scales) + q0 * Shared<NG>::kScales;
+    const uint8_t* points = p.A.zeros + q0 * Shared<NG>::kZeros;
+    int32_t u = static_cast<int32_t>(q0 % units);
+    if (!of_codes) from += static_cast<int64_t>(u) * stage_bytes;
+    int32_t left = static_cast<int32_t>(q1 - q0);
+    int slot = 0, issued = 0;
+    uint32_t phase = 1;
+    for (; left > 0; --left) {
+      if (!mbar_wait(&freed[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&filled[slot], bytes);
         if (of_codes) {
-          // a block's units are consecutive: step q is the matrix's q-th
           uint8_t* to = codes + slot * Shared<NG>::kBytes;
-          bulk_load(to, reinterpret_cast<const uint8_t*>(p.A.codes) + q * Shared<NG>::kCodes, Shared<NG>::kCodes,
-                    &filled[slot]);
-          bulk_load(to + Shared<NG>::kCodes, reinterpret_cast<const uint8_t*>(p.A.scales) + q * Shared<NG>::kScales,
-                    Shared<NG>::kScales, &filled[slot]);
+          bulk_load(to, from, Shared<NG>::kCodes, &filled[slot]);
+          bulk_load(to + Shared<NG>::kCodes, scales, Shared<NG>::kScales, &filled[slot]);
           if (zero_bytes)
-            bulk_load(to + Shared<NG>::kCodes + Shared<NG>::kScales, p.A.zeros + q * Shared<NG>::kZeros, zero_bytes,
-                      &filled[slot]);
+            bulk_load(to + Shared<NG>::kCodes + Shared<NG>::kScales, points, zero_bytes, &filled[slot]);
         } else {
-          bulk_load(tiles + slot * stage_bytes, p.image + static_cast<int64_t>(u) * stage_bytes, stage_bytes,
-                    &filled[slot]);
-          if (++u == units) u = 0;
-        }
-        if (issued < slots) ++issued;
-        if (++slot == slots) {
-          slot = 0;
-          phase ^= 1;
+          bulk_load(tiles + slot * stage_bytes, from, stage_bytes, &filled[slot]);
         }
       }
-      // Copies in flight land before the CTA leaves: a phase ends with its copy, and for the activations with
-      // the unit's weights; when another role has given up only a bounded wait is left to do.
-      for (; issued > 0; --issued) {
-        if (--slot < 0) {
-          slot = slots - 1;
-          phase ^= 1;
+      __syncwarp();
+      if (of_codes) {
+        from += Shared<NG>::kCodes;
+        scales += Shared<NG>::kScales;
+        points += Shared<NG>::kZeros;
+      } else {
+        from += stage_bytes;
+        if (++u == units) {
+          u = 0;
+          from = p.image;
         }
-        mbar_wait_drain(&filled[slot], phase ^ 1, kWaitBudgetNs, p.status);
       }
+      if (issued < slots) ++issued;
+      if (++slot == slots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+    // Copies in flight land before the CTA leaves: a phase ends with its copy, and for the activations with
+    // the unit's weights; when another role has given up only a bounded wait is left to do.
+    for (; issued > 0; --issued) {
+      if (--slot < 0) {
+        slot = slots - 1;
+        phase ^= 1;
+      }
+      mbar_wait_drain(&filled[slot], phase ^ 1, kWaitBudgetNs, p.status);
     }
   }
 
@@ -609,15 +637,14 @@ GemmWorkspace layout(int32_t M, int32_t K, int32_t N) {
   return w;
 }
 
-template <typename T, int NG>
+template <typename T, int NG, int P>
 cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
-  // four units between codes and product where they fit beside as many of codes; the more codes the better:
-  // an SM's share of HBM needs some 35 KB in flight
-  const int32_t tile = p.n_pad * 256;
-  p.slots = p.n_pad <= 128 ? 4 : 3;
-  p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * tile) / Shared<NG>::kBytes)) / p.slots *
-           p.slots;
-  auto kernel = w4_gemm_kernel<T, NG>;
+  // P = 2: four units between codes and product, two to a group of warps, so one is turned into weights while
+  // the products of the other run.  P = 4, for tiles of which only three fit: all warps on each unit.
+  p.slots = P == 2 ? 4 : 3;
+  p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * p.n_pad * 256) / Shared<NG>::kBytes)) / 4 *
+           4 * (P == 2) + 3 * (P == 4);
+  auto kernel = w4_gemm_kernel<T, NG, P>;
   static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -675,15 +702,17 @@ cudaError_t launch_w4_gemm(const flashspmm_w4* in, const void* B, int64_t ldb, v
   if (e != cudaSuccess) return e;
 
   const int64_t ctas = ctas_of(blocks, p.A.units);
-#define FLASHSPMM_BY_GROUP(T)                                  \
-  e = p.A.group == 128  ? launch_as<T, 1>(p, ctas, s)          \
-      : p.A.group == 64 ? launch_as<T, 2>(p, ctas, s)          \
-                        : launch_as<T, 4>(p, ctas, s)
+#define FLASHSPMM_BY_PARTS(T, NG) (p.n_pad <= 128 ? launch_as<T, NG, 2>(p, ctas, s) : launch_as<T, NG, 4>(p, ctas, s))
+#define FLASHSPMM_BY_GROUP(T)                          \
+  e = p.A.group == 128  ? FLASHSPMM_BY_PARTS(T, 1)     \
+      : p.A.group == 64 ? FLASHSPMM_BY_PARTS(T, 2)     \
+                        : FLASHSPMM_BY_PARTS(T, 4)
   if (in->dtype == FLASHSPMM_F16)
     FLASHSPMM_BY_GROUP(__half);
   else
     FLASHSPMM_BY_GROUP(__nv_bfloat16);
 #undef FLASHSPMM_BY_GROUP
+#undef FLASHSPMM_BY_PARTS
   note_launch();
   return e;
 }

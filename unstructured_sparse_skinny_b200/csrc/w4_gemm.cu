@@ -50,7 +50,7 @@ struct GemmParams {
   bool c_f32;
   int32_t N, n_pad;
   int32_t slots, ring;
-  int64_t steps;         // blocks * units
+  int32_t steps;         // blocks * units
   int* status;
 };
 
@@ -249,37 +249,38 @@ struct Accumulators {
 
 // A run of steps cut into segments of one block each.
 struct Segment {
-  int64_t block;
-  int64_t from, to;  // steps
+  int32_t block;
+  int32_t from, to;  // steps
   bool whole;
 };
-__device__ __forceinline__ Segment segment_at(int64_t q, int64_t end, int32_t units) {
+__device__ __forceinline__ Segment segment_of(int32_t block, int32_t q0, int32_t q1, int32_t units) {
   Segment s;
-  s.block = q / units;
-  s.from = q;
-  s.to = min64(end, (s.block + 1) * units);
+  s.block = block;
+  s.from = max(q0, block * units);
+  s.to = min(q1, (block + 1) * units);
   s.whole = s.to - s.from == units;
   return s;
 }
-__host__ __device__ __forceinline__ int64_t run_begin(int64_t steps, int64_t cta, int64_t ctas) {
-  return steps * cta / ctas;
-}
-// The CTA whose run holds step q.
-__device__ __forceinline__ int64_t run_owner(int64_t steps, int64_t q, int64_t ctas) {
-  int64_t c = q * ctas / steps;
-  while (run_begin(steps, c + 1, ctas) <= q) ++c;
-  while (run_begin(steps, c, ctas) > q) --c;
-  return c;
-}
+
+// Runs differ by a step at most, the longer ones first.
+struct Runs {
+  int32_t base, longer;
+  __device__ __forceinline__ Runs(int32_t steps, int32_t ctas) : base(steps / ctas), longer(steps % ctas) {}
+  __device__ __forceinline__ int32_t begin(int32_t cta) const { return cta * base + min(cta, longer); }
+  __device__ __forceinline__ int32_t owner(int32_t q) const {
+    const int32_t head = longer * (base + 1);
+    return q < head ? q / (base + 1) : longer + (q - head) / base;
+  }
+};
 
 // The accumulators of a segment to C (a whole block) or to the CTA's slot of
 // the workspace, by `groups` warps per 32 rows, this one the `group`-th.
 template <typename T>
 __device__ __forceinline__ void drain_segment(const GemmParams& p, const Segment& seg, const Accumulators& acc,
-                                              uint32_t tmem, int buffer, int64_t q0, int group, int groups, int quad,
+                                              uint32_t tmem, int buffer, int32_t q0, int group, int groups, int quad,
                                               int lane) {
   const int row = quad * 32 + lane;
-  const int64_t m = seg.block * kBlockRows + row;
+  const int64_t m = static_cast<int64_t>(seg.block) * kBlockRows + row;
   const uint32_t from = tmem + acc.at(0, buffer) + (static_cast<uint32_t>(quad * 32) << 16);
   const int first = static_cast<int>((seg.from - q0) & 1);
   // with two issuers: a segment of one unit has one sum, in its issuer's accumulator
@@ -307,19 +308,29 @@ __device__ __forceinline__ void drain_segment(const GemmParams& p, const Segment
 
 // The CTAs that share a block.
 struct Sharers {
-  int64_t first, last;
-  int64_t first_slot;  // the others hold the block first in their run
-  __device__ __forceinline__ Sharers(const GemmParams& p, int64_t block) {
-    const int64_t from = block * p.A.units;
-    first = run_owner(p.steps, from, gridDim.x);
-    last = run_owner(p.steps, from + p.A.units - 1, gridDim.x);
-    first_slot = first * 2 + (run_begin(p.steps, first, gridDim.x) < from);
+  int32_t first, last;
+  int32_t first_slot;  // the others hold the block first in their run
+  __device__ __forceinline__ Sharers(const Runs& runs, int32_t block, int32_t units) {
+    const int32_t from = block * units;
+    first = runs.owner(from);
+    last = runs.owner(from + units - 1);
+    first_slot = first * 2 + (runs.begin(first) < from);
   }
 };
 
+// One thread's call after a barrier of the block's warps: whether this CTA is
+// the last of the block's to have its sums in the workspace.  The fences cover
+// what the barrier ordered before them, and what follows the next one.
+__device__ __forceinline__ bool arrive_at(const GemmParams& p, int32_t block, const Sharers& who) {
+  __threadfence();
+  const bool last = atomicAdd(&p.arrived[block], 1) == who.last - who.first;
+  __threadfence();
+  return last;
+}
+
 // All sums of a shared block, in the order of its CTAs, by `threads` threads.
 template <typename T>
-__device__ __forceinline__ void join_block(const GemmParams& p, int64_t block, const Sharers& who, int tid,
+__device__ __forceinline__ void join_block(const GemmParams& p, int32_t block, const Sharers& who, int tid,
                                            int threads) {
   constexpr int kBatch = 4;  // loads in flight a thread and CTA
   const int32_t total = p.N * (kBlockRows / 4);
@@ -327,9 +338,9 @@ __device__ __forceinline__ void join_block(const GemmParams& p, int64_t block, c
   const int64_t slot = static_cast<int64_t>(p.n_pad) * (kBlockRows / 4);
   for (int32_t i0 = tid; i0 < total; i0 += threads * kBatch) {
     float4 sum[kBatch] = {};
-    for (int64_t c = who.first; c <= who.last; c += 2) {
+    for (int32_t c = who.first; c <= who.last; c += 2) {
       const float4* s0 = base + (c == who.first ? who.first_slot : c * 2) * slot;
-      const float4* s1 = base + (c + 1) * 2 * slot;
+      const float4* s1 = base + static_cast<int64_t>(c + 1) * 2 * slot;
       const bool second = c < who.last;
       float4 v0[kBatch], v1[kBatch];
 #pragma unroll
@@ -349,7 +360,7 @@ __device__ __forceinline__ void join_block(const GemmParams& p, int64_t block, c
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int32_t i = i0 + threads * j;
-      if (i < total) store_four<T>(p, i / (kBlockRows / 4), block * kBlockRows + (i % (kBlockRows / 4)) * 4, sum[j]);
+      if (i < total) store_four<T>(p, i / (kBlockRows / 4), static_cast<int64_t>(block) * kBlockRows + (i % (kBlockRows / 4)) * 4, sum[j]);
     }
   }
 }
@@ -364,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t units = p.A.units;
-  const int64_t q0 = run_begin(p.steps, blockIdx.x, gridDim.x), q1 = run_begin(p.steps, blockIdx.x + 1, gridDim.x);
+  const Runs runs(p.steps, gridDim.x);
+  const int32_t q0 = runs.begin(blockIdx.x), q1 = runs.begin(blockIdx.x + 1);
   const uint32_t stage_bytes = static_cast<uint32_t>(p.n_pad) * 256;
   const Accumulators acc(p.n_pad);
   uint8_t* tiles = smem + ((1024 - (smem_u32(smem) & 1023)) & 1023);
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     const bool zeros = p.A.zeros != nullptr;
     uint32_t phase = 1, ring_phase = 0;
     int ring = group, slot = group;
-    for (int64_t q = q0 + group; q < q1; q += kGroups) {
+    for (int32_t q = q0 + group; q < q1; q += kGroups) {
       if (!mbar_wait(&codes_full[ring], ring_phase, abort_flag, kWaitBudgetNs, p.status)) break;
       __syncwarp();
       uint32_t r[2][32 / P];
@@ -442,10 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     griddep_wait();
     int buffer = 0;
     uint32_t phase = 0;
-    for (int64_t q = q0;;) {
-      const Segment seg = segment_at(q, q1, units);
-      if (seg.to == q1) break;
-      q = seg.to;
+    for (int32_t block = q0 / units; (block + 1) * units < q1; ++block) {
+      const Segment seg = segment_of(block, q0, q1, units);
+      const Sharers who(runs, block, units);
       // a wait that runs out leaves wrong values and an error, not a warp missing at the barriers below
       mbar_wait(&acc_full[buffer], phase, abort_flag, kWaitBudgetNs, p.status);
       __syncwarp();
@@ -459,14 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
         phase ^= 1;
       }
       if (seg.whole) continue;
-      const Sharers who(p, seg.block);
-      __threadfence();
       named_barrier(1, 128);
-      if (warp == kEpilogueWarp && lane == 0)
-        last_word = atomicAdd(&p.arrived[seg.block], 1) == static_cast<int32_t>(who.last - who.first);
+      if (warp == kEpilogueWarp && lane == 0) last_word = arrive_at(p, seg.block, who);
       named_barrier(1, 128);
       if (!last_word) continue;
-      __threadfence();
       join_block<T>(p, seg.block, who, threadIdx.x - kEpilogueWarp * 32, 128);
     }
   } else if (warp < kLoadWarp) {
@@ -477,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
       const uint32_t idesc = idesc_of<T>(p.n_pad);
       const uint64_t desc0 = smem_desc_k_sw128(smem_u32(tiles));
       const uint32_t half = stage_bytes / 2 / 16;  // descriptor addresses count 16 bytes
-      int32_t left = static_cast<int32_t>(min64(q1 - q0, units - q0 % units));  // steps of the current segment
-      int64_t rest = q1 - q0;
+      int32_t left = min(q1 - q0, units - q0 % units);  // steps of the current segment
+      int32_t rest = q1 - q0;
       int slot = me, buffer = 0, skip = me;  // steps until the next one of this warp
       uint32_t phase = 0, acc_phase = 1;
       bool dead = false;
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
           buffer = 0;
           acc_phase ^= 1;
         }
-        left = static_cast<int32_t>(min64(rest, units));
+        left = min(rest, units);
       }
       if (elect_one()) umma_commit(&mma_done[me]);
     }
@@ -534,12 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     const uint32_t zero_bytes = p.A.zeros ? Shared<NG>::kZeros : 0;
     const uint32_t bytes = of_codes ? Shared<NG>::kCodes + Shared<NG>::kScales + zero_bytes : stage_bytes;
     // a block's units are consecutive: step q is the matrix's q-th
-    const uint8_t* from = of_codes ? reinterpret_cast<const uint8_t*>(p.A.codes) + q0 * Shared<NG>::kCodes : p.image;
-    const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.A.scales) + q0 * Shared<NG>::kScales;
-    const uint8_t* points = p.A.zeros + q0 * Shared<NG>::kZeros;
-    int32_t u = static_cast<int32_t>(q0 % units);
+    const int64_t first = q0;
+    const uint8_t* from =
+        of_codes ? reinterpret_cast<const uint8_t*>(p.A.codes) + first * Shared<NG>::kCodes : p.image;
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.A.scales) + first * Shared<NG>::kScales;
+    const uint8_t* points = p.A.zeros + first * Shared<NG>::kZeros;
+    int32_t u = q0 % units;
     if (!of_codes) from += static_cast<int64_t>(u) * stage_bytes;
-    int32_t left = static_cast<int32_t>(q1 - q0);
+    int32_t left = q1 - q0;
     int slot = 0, issued = 0;
     uint32_t phase = 1;
     for (; left > 0; --left) {
@@ -588,28 +597,25 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   // ---- the run's last block, by all warps.  (They wait for the end of all products: a phase of acc_full
   // could still be two ahead of a warp that comes here early, which parity does not tell from none.)
   __syncwarp();
-  const int64_t last_block = (q1 - 1) / units, before = last_block - q0 / units;
-  const Segment seg = segment_at(max64(q0, last_block * units), q1, units);
-  const int buffer = static_cast<int>(before % acc.buffers);
+  const int32_t last_block = (q1 - 1) / units, before = last_block - q0 / units;
+  const Segment seg = segment_of(last_block, q0, q1, units);
+  const Sharers who(runs, last_block, units);
+  const int buffer = before % acc.buffers;
   griddep_wait();
   for (int i = 0; i < acc.issuers; ++i) mbar_wait_drain(&mma_done[i], 0, kWaitBudgetNs, p.status);
   __syncwarp();
   tc_fence_after_sync();
   if (warp < kMmaWarp) drain_segment<T>(p, seg, acc, tmem, buffer, q0, warp >> 2, kMmaWarp / 4, warp & 3, lane);
   tc_fence_before_sync();
-  if (!seg.whole) __threadfence();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
   if (seg.whole) return;
-  const Sharers who(p, seg.block);
-  if (threadIdx.x == 0)
-    last_word = atomicAdd(&p.arrived[seg.block], 1) == static_cast<int32_t>(who.last - who.first);
+  if (threadIdx.x == 0) last_word = arrive_at(p, seg.block, who);
   __syncthreads();
   if (!last_word) return;
-  __threadfence();
   join_block<T>(p, seg.block, who, threadIdx.x, kThreads);
 }
 
@@ -688,7 +694,8 @@ cudaError_t launch_w4_gemm(const flashspmm_w4* in, const void* B, int64_t ldb, v
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInitializationError;
   const int64_t blocks = (static_cast<int64_t>(p.A.M) + kBlockRows - 1) / kBlockRows;
-  p.steps = blocks * p.A.units;
+  if (blocks * p.A.units > INT32_MAX) return cudaErrorInvalidValue;  // 16 TB of codes
+  p.steps = static_cast<int32_t>(blocks * p.A.units);
 
   const int64_t k_blocks = static_cast<int64_t>(p.A.units) * 4;
   const dim3 grid(static_cast<unsigned>((k_blocks * p.n_pad + 255) / 256));

@@ -14,7 +14,7 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 SOURCES = [PKG / "csrc" / f for f in ("flashspmm_api.cu", "tcsl_encode.cu", "spmm_lscd.cu", "spmm_noalloc.cu", "partition.cu", "round_f16.cu", "selftest.cu",
                                       "w4_api.cu", "w4_format.cu", "w4_matmul.cu", "w4_gemm.cu", "moe_w4.cu")]
-DEPS = SOURCES + [PKG / "csrc" / f for f in ("common.cuh", "sm100_primitives.cuh", "w4.cuh")] + [ROOT / "include" / "flashspmm.h"]
+DEPS = SOURCES + [PKG / "csrc" / f for f in ("common.cuh", "sm100_primitives.cuh", "w4.cuh", "w4_strips.cuh")] + [ROOT / "include" / "flashspmm.h"]
 LIB = PKG / "libflashspmm.so"
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "0"]

@@ -5,17 +5,21 @@
 //   h_e    = act(gate_e x) * (up_e x), or act(gate_e x)
 //   out    = sum over the token's experts of p * (down_e h_e)
 //
-// Four kernels: logits; routing, which turns the choice into one list of
-// tokens per running expert; gate and up with the activation; down with the
-// weighted sum.  Every expert's codes are read once however many of its tokens
-// there are, and every sum has a fixed order: no atomics on values.
-#include "w4.cuh"
+// Five kernels, each started while the one before it ends: logits; routing,
+// which turns the choice into one list of tokens per running expert; gate and
+// up with the activation; down, weighted; and the sum over a token's experts.
+// Every expert's codes are read once however many of its tokens there are, and
+// every sum has a fixed order: no atomics on values.
+#include <atomic>
+
+#include "w4_strips.cuh"
 
 namespace flashspmm {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kRouteThreads = 512;
+constexpr int kRouteWarps = 16;
+constexpr int kRouteThreads = kRouteWarps * 32;
+constexpr int kRouteCtas = 8;  // one cluster
 
 // An expert that runs: its tokens are pairs [first, first + count).
 struct __align__(16) Slot {
@@ -23,13 +27,15 @@ struct __align__(16) Slot {
 };
 
 struct Workspace {
-  Slot* slots;         // [E], the first *running of them in use
+  Slot* slots;           // [E], the first *running of them in use
   int32_t* running;
-  int32_t* pair_token; // [T * top_k], by expert, tokens ascending
+  int32_t* pair_token;   // [T * top_k], by expert, tokens ascending
   float* pair_weight;
-  double* logits;      // [T][E]
-  uint16_t* h;         // [T * top_k][ldh]
-  uint16_t* x;         // aligned copy of the activations, if one is needed
+  int32_t* place;        // [T][top_k]: the pair of a token's j-th expert, -1 where there is none
+  double* logits;        // [T][E]
+  uint16_t* h;           // [T * top_k][ldh]
+  float* y;              // [T * top_k][H], weighted
+  uint16_t* x;           // aligned copy of the activations, if one is needed
   int64_t ldh;
   size_t bytes;
 };
@@ -50,8 +56,10 @@ Workspace carve(void* base, int32_t T, int32_t E, int32_t top_k, int32_t H, int3
   w.running = reinterpret_cast<int32_t*>(take(4));
   w.pair_token = reinterpret_cast<int32_t*>(take(4 * pairs));
   w.pair_weight = reinterpret_cast<float*>(take(4 * pairs));
+  w.place = reinterpret_cast<int32_t*>(take(4 * pairs));
   w.logits = reinterpret_cast<double*>(take(sizeof(double) * T * E));
   w.h = reinterpret_cast<uint16_t*>(take(2 * pairs * w.ldh));
+  w.y = reinterpret_cast<float*>(take(sizeof(float) * pairs * H));
   w.x = reinterpret_cast<uint16_t*>(take(aligned ? 0 : static_cast<size_t>(T) * aligned_k(H) * 2));
   w.bytes = o;
   return w;
@@ -94,97 +102,123 @@ struct RouterRow<float> {
   }
 };
 
-// One warp per expert and four tokens.  Equal router rows give equal logits
-// bit for bit: the order of a sum depends on H alone.
-template <typename T, typename RT, bool Vec>
-__global__ void __launch_bounds__(kWarps * 32) moe_logits_kernel(const uint16_t* __restrict__ X, int64_t ldx,
-                                                                 const void* __restrict__ router, int32_t H,
-                                                                 int32_t tokens, int32_t E,
-                                                                 double* __restrict__ logits) {
-  const int lane = threadIdx.x & 31;
-  const int32_t e = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int32_t t0 = blockIdx.y * 4;
-  if (e >= E) return;
-  double acc[4] = {};
-  for (int32_t k = 8 * lane; k < H; k += 256) {
-    float w[8];
-    RouterRow<RT>::template load<Vec>(router, e, k, H, w);
+// A CTA has EB experts and TB tokens; its threads share the columns, eight
+// neighbours each.  A conversion to 64 bits costs four fused multiply-adds of
+// the same width, so a thread converts once for EB or TB products.  Equal
+// router rows give equal logits bit for bit: the order of a sum depends on H
+// and the tile's shape alone.
+template <typename T, typename RT, bool Vec, int EB, int TB>
+__global__ void __launch_bounds__(256) moe_logits_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                         const void* __restrict__ router, int32_t H, int32_t tokens,
+                                                         int32_t E, double* __restrict__ logits) {
+  __shared__ double part[8][EB * TB];
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
+  double acc[EB][TB] = {};
+  for (int32_t k = 8 * threadIdx.x; k < H; k += 2048) {
+    float w[EB][8], x[TB][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x[8];
-      // rows are padded to 8 values with zeros, so this load needs no check of H
-      unpack8<T>(load_act8<true>(t0 + j < tokens ? X + (t0 + j) * ldx : nullptr, k, H), x);
+    for (int i = 0; i < EB; ++i) RouterRow<RT>::template load<Vec>(router, min(e0 + i, E - 1), k, H, w[i]);
+    // rows are padded to 8 values, and the router's values behind H are zeros
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[j] = fma(static_cast<double>(w[i]), static_cast<double>(x[i]), acc[j]);
+    for (int j = 0; j < TB; ++j) unpack8<T>(load_act8<true>(X + min(t0 + j, tokens - 1) * ldx, k, H), x[j]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      double wd[EB], xd[TB];
+#pragma unroll
+      for (int i = 0; i < EB; ++i) wd[i] = w[i][c];
+#pragma unroll
+      for (int j = 0; j < TB; ++j) xd[j] = x[j][c];
+#pragma unroll
+      for (int i = 0; i < EB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = fma(wd[i], xd[j], acc[i][j]);
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int i = 0; i < EB; ++i)
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], m);
-    if (lane == 0 && t0 + j < tokens) logits[static_cast<int64_t>(t0 + j) * E + e] = acc[j];
+    for (int j = 0; j < TB; ++j) {
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) acc[i][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[i][j], m);
+      if (lane == 0) part[warp][i * TB + j] = acc[i][j];
+    }
+  __syncthreads();
+  if (threadIdx.x < EB * TB) {
+    const int32_t e = e0 + threadIdx.x / TB, t = t0 + threadIdx.x % TB;
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += part[w][threadIdx.x];
+    if (e < E && t < tokens) logits[static_cast<int64_t>(t) * E + e] = sum;
   }
 }
 
 // ---------------------------------------------------------------- routing
 
-// The top_k of one token by one warp.  A NaN counts as the lowest value, so
-// the chosen experts are always top_k different ones; its token's weights are
-// NaN.
+// Whole numbers in the order of the values.  A NaN counts as the lowest.
+__device__ __forceinline__ unsigned long long sort_key(double v) {
+  v += 0.0;  // -0 is 0
+  const unsigned long long b = __double_as_longlong(v);
+  return v != v ? 0ull : b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_value(unsigned long long k) {
+  return __longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+}
+
+// The top_k of one token by one warp, 32 * Per experts at most.  The chosen
+// experts are always top_k different ones; the weights of a token with a NaN
+// among its logits are NaN.
+template <int Per>
 __device__ __forceinline__ void top_k_of(const double* logits, int32_t E, int32_t top_k, bool renormalize, int lane,
                                          int32_t* ids, float* weights) {
-  constexpr int kPer = kMoeMaxExperts / 32;
-  const double lowest = -__longlong_as_double(0x7FF0000000000000ll);
-  double v[kPer];
+  // 0 marks what is behind E or taken; the lowest value (and NaN) counts as 1
+  unsigned long long key[Per];
   bool nan = false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < Per; ++i) {
     const int32_t e = lane + 32 * i;
-    v[i] = e < E ? logits[e] : lowest;
-    if (v[i] != v[i]) {
-      nan = true;
-      v[i] = lowest;
-    }
+    const double v = e < E ? logits[e] : 0.0;
+    nan |= v != v;
+    key[i] = e < E ? max(sort_key(v), 1ull) : 0ull;
   }
   nan = __any_sync(0xFFFFFFFFu, nan);
-  uint32_t used = 0;
+  unsigned long long rest[Per];
+#pragma unroll
+  for (int i = 0; i < Per; ++i) rest[i] = key[i];
   double top = 0.0;
   int32_t my_id = 0;
   float my_e = 0.0f, sum = 0.0f;
   for (int32_t j = 0; j < top_k; ++j) {
-    double best = lowest;
-    int32_t at = INT32_MAX;
+    unsigned long long best = rest[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int32_t e = lane + 32 * i;
-      if (e < E && !(used >> i & 1) && (at == INT32_MAX || v[i] > best)) {
-        best = v[i];
-        at = e;
-      }
-    }
+    for (int i = 1; i < Per; ++i) best = max(best, rest[i]);
+    const uint32_t high = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(best >> 32));
+    const uint32_t low = __reduce_max_sync(
+        0xFFFFFFFFu, static_cast<uint32_t>(best >> 32) == high ? static_cast<uint32_t>(best) : 0u);
+    const unsigned long long taken = (static_cast<unsigned long long>(high) << 32) | low;
+    uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-      const double ov = __shfl_xor_sync(0xFFFFFFFFu, best, m);
-      const int32_t oe = __shfl_xor_sync(0xFFFFFFFFu, at, m);
-      if (ov > best || (ov == best && oe < at)) {
-        best = ov;
-        at = oe;
-      }
-    }
-    if (j == 0) top = best;
-    if ((at & 31) == lane) used |= 1u << (at >> 5);
-    const float e = expf(static_cast<float>(best - top));
+    for (int i = Per - 1; i >= 0; --i)
+      if (rest[i] == taken) at = lane + 32 * i;
+    at = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+    for (int i = 0; i < Per; ++i)
+      if (lane + 32 * i == static_cast<int32_t>(at)) rest[i] = 0;
+    const double value = key_value(taken);
+    if (j == 0) top = value;
+    const float e = expf(static_cast<float>(value - top));
     sum += e;
     if (lane == j) {
-      my_id = at;
+      my_id = static_cast<int32_t>(at);
       my_e = e;
     }
   }
   if (!renormalize) {
     sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < E) sum += expf(static_cast<float>(v[i] - top));
+    for (int i = 0; i < Per; ++i)
+      if (lane + 32 * i < E) sum += expf(static_cast<float>(key_value(key[i]) - top));
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
   }
@@ -194,42 +228,61 @@ __device__ __forceinline__ void top_k_of(const double* logits, int32_t E, int32_
   }
 }
 
-// One CTA: the choice (or the caller's), then for every expert the set of its
-// tokens as 64 bits, their counts' running sum, and the lists.  An id outside
-// 0 .. E - 1 contributes nothing; one that a token names twice runs once with
-// the sum of its weights.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// (The barrier before it brings a warp's lanes together: an .aligned arrival counts for the whole warp, also
+// while one of its lanes is still in a branch.)
+__device__ __forceinline__ void cluster_sync() {
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared-memory address in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+
+// A cluster: a warp per token chooses (or takes the caller's choice) and sets
+// the token's bit in its experts' sets, which the first CTA holds; then that
+// CTA makes the running experts' lists: their sizes' running sum, and a pair's
+// place in its list from the bits below its own.  An id outside 0 .. E - 1
+// contributes nothing; one that a token names twice runs once with the sum of
+// its weights.
+template <int Per>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(bool given, int32_t tokens, int32_t E, int32_t top_k,
                                                                   bool renormalize, int32_t* ids, float* weights,
                                                                   Workspace ws) {
-  __shared__ int32_t s_ids[kMoeMaxTokens * kMoeMaxTopK];
-  __shared__ float s_weights[kMoeMaxTokens * kMoeMaxTopK];
   __shared__ unsigned long long mask[kMoeMaxExperts];
-  __shared__ int32_t part[kRouteThreads / 32][2];
+  __shared__ int32_t start[kMoeMaxExperts];
+  __shared__ int32_t part[kRouteWarps][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
   mask[tid] = 0;
-  const int32_t pairs = tokens * top_k;
-  if (given) {
-    for (int i = tid; i < pairs; i += kRouteThreads) {
-      s_ids[i] = ids[i];
-      s_weights[i] = weights[i];
-    }
-  } else {
-    for (int32_t t = warp; t < tokens; t += kRouteThreads / 32)
-      top_k_of(ws.logits + static_cast<int64_t>(t) * E, E, top_k, renormalize, lane, s_ids + t * top_k,
-               s_weights + t * top_k);
-  }
-  __syncthreads();
-  for (int i = tid; i < pairs; i += kRouteThreads) {
-    const int32_t e = s_ids[i];
-    if (e >= 0 && e < E) atomicOr(&mask[e], 1ull << (i / top_k));
-    if (!given) {
-      ids[i] = e;
-      weights[i] = s_weights[i];
+  griddep_wait();
+  griddep_launch_dependents();
+  cluster_sync();
+  for (int32_t t = rank + kRouteCtas * warp; t < tokens; t += kRouteCtas * kRouteWarps) {
+    if (!given)
+      top_k_of<Per>(ws.logits + static_cast<int64_t>(t) * E, E, top_k, renormalize, lane, ids + t * top_k,
+                    weights + t * top_k);
+    __syncwarp();
+    if (lane < top_k) {
+      const int32_t e = ids[t * top_k + lane];
+      if (e >= 0 && e < E)
+        // in halves of 32 bits: the 64-bit form lost bits that two CTAs set at the same time
+        asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(in_first_cta(&mask[e]) + (t >> 5) * 4),
+                     "r"(1u << (t & 31))
+                     : "memory");
     }
   }
-  __syncthreads();
-  unsigned long long mine = tid < E ? mask[tid] : 0;
-  const int32_t count = __popcll(mine), runs = count > 0;
+  __threadfence();
+  cluster_sync();
+  if (rank != 0) return;
+  const int32_t count = tid < E ? __popcll(mask[tid]) : 0, runs = count > 0;
   int32_t first = count, slot = runs;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -244,216 +297,222 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(bool given, in
     part[warp][1] = slot;
   }
   __syncthreads();
-  int32_t before0 = 0, before1 = 0;
   for (int w = 0; w < warp; ++w) {
-    before0 += part[w][0];
-    before1 += part[w][1];
+    first += part[w][0];
+    slot += part[w][1];
   }
-  first += before0 - count;
-  slot += before1 - runs;
-  if (tid == kRouteThreads - 1) *ws.running = slot + runs;
-  if (!runs) return;
-  ws.slots[slot] = Slot{tid, first, count, 0};
-  for (int32_t i = 0; i < count; ++i) {
-    const int32_t t = __ffsll(static_cast<long long>(mine)) - 1;
-    mine &= mine - 1;
-    float w = 0.0f;
-    for (int32_t j = 0; j < top_k; ++j)
-      if (s_ids[t * top_k + j] == tid) w += s_weights[t * top_k + j];
-    ws.pair_token[first + i] = t;
-    ws.pair_weight[first + i] = w;
+  start[tid] = first - count;
+  if (tid == kRouteThreads - 1) *ws.running = slot;
+  if (runs) ws.slots[slot - 1] = Slot{tid, first - count, count, 0};
+  __syncthreads();
+  for (int32_t i = tid; i < tokens * top_k; i += kRouteThreads) {
+    const int32_t t = i / top_k, e = __ldcg(ids + i);
+    int32_t place = -1;
+    if (e >= 0 && e < E) {
+      const int32_t at = start[e] + __popcll(mask[e] & ((1ull << t) - 1));
+      float w = 0.0f;
+      bool again = false;  // a token's sum counts an expert's pair once
+      for (int32_t j = 0; j < top_k; ++j)
+        if (__ldcg(ids + t * top_k + j) == e) {
+          w += __ldcg(weights + t * top_k + j);
+          again |= t * top_k + j < i;
+        }
+      ws.pair_token[at] = t;
+      ws.pair_weight[at] = w;
+      if (!again) place = at;
+    }
+    ws.place[i] = place;
   }
 }
 
-// ---------------------------------------------------------------- gate and up
+// ---------------------------------------------------------------- experts
 
 __device__ __forceinline__ float activate(int kind, float v) {
   if (kind == FLASHSPMM_ACT_SILU) return v / (1.0f + expf(-v));
   if (kind == FLASHSPMM_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-  return fmaxf(v, 0.0f) + (v != v ? v : 0.0f);  // relu, NaN kept
+  return v < 0.0f ? 0.0f : v;  // relu, NaN kept
 }
 
-// h[pair][f] for one strip of 16 rows f of one running expert.  h is rounded
+struct ExpertParams {
+  W4Dev gate, up;        // up.codes null: no gate product
+  W4Dev down;
+  const uint16_t* X;
+  int64_t ldx;
+  int32_t H;             // columns of X that may be read
+  int32_t activation;
+  int32_t pairs;         // of strips a CTA
+  uint32_t shared;
+  Workspace ws;
+};
+
+// h[pair][f] for some strips of 16 rows f of a running expert.  h is rounded
 // to the activations' type: it is the next product's tensor-core operand.
-template <typename T, int NG, int R, int NT>
-__global__ void __launch_bounds__(kWarps * 32) moe_gate_up_kernel(W4Dev gate, W4Dev up, const uint16_t* __restrict__ X,
-                                                                  int64_t ldx, int32_t H, int activation,
-                                                                  Workspace ws) {
-  constexpr int kPass = NT < 2 ? NT : 2;  // tiles added up at a time, for the size of `red`
-  constexpr int kRows = 16 * R, kPitch = kRows + 4;
-  __shared__ float red[kWarps][kPass * 8][kPitch];
-  __shared__ int32_t tok[kMoeMaxTokens];
-  if (static_cast<int32_t>(blockIdx.y) >= *ws.running) return;
-  const Slot slot = ws.slots[blockIdx.y];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (threadIdx.x < slot.count) tok[threadIdx.x] = ws.pair_token[slot.first + threadIdx.x];
-  __syncthreads();
-  const int tiles = (slot.count + 7) / 8;
-  float acc[R][NT][4] = {};
-  const auto act = [&](int nt, int32_t k) {
-    const int n = 8 * nt + g;
-    return load_act8<true>(n < slot.count ? X + tok[n] * ldx : nullptr, k + 8 * t, H);
-  };
-  for (int32_t u = warp; u < gate.units; u += kWarps) {
-    uint4 c[R][2];
-    W4Groups<T, NG> grp[R];
-    const int64_t unit = gate.unit(slot.expert, blockIdx.x, u);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const W4Dev& A = r ? up : gate;
-      c[r][0] = ld_stream(A.codes + unit * 64 + lane);
-      c[r][1] = ld_stream(A.codes + unit * 64 + 32 + lane);
-      grp[r].load(A, unit, g);
-    }
-    w4_unit<T, NG, R, NT>(c, grp, u * kW4UnitCols, tiles, act, acc);
-  }
-#pragma unroll
-  for (int p = 0; p < NT / kPass; ++p) {
-    if (p * kPass >= tiles) break;
-    if (p > 0) __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int nt = 0; nt < kPass; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          red[warp][nt * 8 + 2 * t + (i & 1)][r * 16 + g + 8 * (i >> 1)] = acc[r][p * kPass + nt][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < kPass * 8 * 16; i += kWarps * 32) {
-      const int n = i >> 4, row = i & 15;
-      const int32_t pair = p * kPass * 8 + n, f = blockIdx.x * 16 + row;
-      if (pair >= slot.count || f >= ws.ldh) continue;
-      float v = 0.0f, u = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        v += red[w][n][row];
-        if (R == 2) u += red[w][n][16 * (R - 1) + row];
-      }
-      v = activate(activation, v);
-      if (R == 2) v *= u;
+template <typename T, int NG, int NT>
+__global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_kernel(const ExpertParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int32_t token[kMoeMaxTokens];
+  griddep_wait();
+  griddep_launch_dependents();
+  if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
+  const Slot slot = p.ws.slots[blockIdx.y];
+  const bool gated = p.up.codes != nullptr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t strip0 = blockIdx.x * p.pairs;
+  const int64_t unit = p.gate.unit(slot.expert, min(strip0 + warp % p.pairs, p.gate.strips - 1), 0);
+  // without a gate product the second strip is the first again, and its sums are not used
+  const StripAt at[2] = {StripAt(p.gate, unit, lane), StripAt(gated ? p.up : p.gate, unit, lane)};
+  if (threadIdx.x < slot.count) token[threadIdx.x] = p.ws.pair_token[slot.first + threadIdx.x];
+  for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
+    const int32_t rows = min(slot.count - n0, NT * 8);
+    float acc[2][NT][4] = {};
+    strip_product<T, NG, NT>(
+        at, p.gate.units, p.H, rows, p.pairs, smem, p.shared,
+        [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
+    strip_reduce<NT, true>(acc, p.pairs, rows, smem, [&](int pair, int32_t n, int32_t row, float g, float u) {
+      const int32_t f = (strip0 + pair) * 16 + row;
+      if (f >= p.ws.ldh) return;
+      const float v = activate(p.activation, g) * (gated ? u : 1.0f);
       // columns behind F pad h to 16 bytes: finite whatever x holds
-      reinterpret_cast<T*>(ws.h)[(slot.first + pair) * ws.ldh + f] = from_float<T>(f < gate.M ? v : 0.0f);
-    }
+      reinterpret_cast<T*>(p.ws.h)[(slot.first + n0 + n) * p.ws.ldh + f] = from_float<T>(f < p.gate.M ? v : 0.0f);
+    });
   }
 }
 
-// ---------------------------------------------------------------- down
-
-// out[.][strip of 16 rows]: the warps share all units of all running experts
-// in runs; at an expert's end a warp adds its weighted sums to its own table
-// of tokens, and the tables are added in a fixed order.
+// y[pair] = weight * down h for some pairs of strips of a running expert.
 template <typename T, int NG, int NT>
-__global__ void __launch_bounds__(kWarps * 32) moe_down_kernel(W4Dev A, int32_t tokens, T* __restrict__ out,
-                                                               int64_t ldo, Workspace ws) {
-  constexpr int kPitch = 16 + 4;
-  __shared__ float sum[kWarps][NT * 8][kPitch];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  for (int i = threadIdx.x; i < kWarps * NT * 8 * kPitch; i += kWarps * 32) (&sum[0][0][0])[i] = 0.0f;
-  __syncthreads();
-  const int32_t ldh = static_cast<int32_t>(ws.ldh);
-  const int64_t items = static_cast<int64_t>(*ws.running) * A.units;
-  int64_t i = items * warp / kWarps;
-  const int64_t end = items * (warp + 1) / kWarps;
-  while (i < end) {
-    const int32_t s = static_cast<int32_t>(i / A.units);
-    const Slot slot = ws.slots[s];
-    const int64_t stop = min64(end, static_cast<int64_t>(s + 1) * A.units);
-    const int tiles = (slot.count + 7) / 8;
-    const int64_t unit0 = A.unit(slot.expert, blockIdx.x, 0);
-    float acc[1][NT][4] = {};
-    const auto act = [&](int nt, int32_t k) {
-      const int n = 8 * nt + g;
-      return load_act8<true>(n < slot.count ? ws.h + (slot.first + n) * ws.ldh : nullptr, k + 8 * t, ldh);
-    };
-    for (; i < stop; ++i) {
-      const int32_t u = static_cast<int32_t>(i - static_cast<int64_t>(s) * A.units);
-      uint4 c[1][2];
-      W4Groups<T, NG> grp[1];
-      const int64_t unit = unit0 + 8 * static_cast<int64_t>(u);
-      c[0][0] = ld_stream(A.codes + unit * 64 + lane);
-      c[0][1] = ld_stream(A.codes + unit * 64 + 32 + lane);
-      grp[0].load(A, unit, g);
-      w4_unit<T, NG, 1, NT>(c, grp, u * kW4UnitCols, tiles, act, acc);
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = nt * 8 + 2 * t + j;
-        if (n < slot.count) {
-          const int32_t token = ws.pair_token[slot.first + n];
-          const float w = ws.pair_weight[slot.first + n];
-          sum[warp][token][g] = fmaf(w, acc[0][nt][j], sum[warp][token][g]);
-          sum[warp][token][g + 8] = fmaf(w, acc[0][nt][2 + j], sum[warp][token][g + 8]);
-        }
-      }
-    __syncwarp();  // the next expert's lanes hold other tokens
-  }
-  __syncthreads();
-  for (int o = threadIdx.x; o < tokens * 16; o += kWarps * 32) {
-    const int token = o >> 4, row = o & 15;
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + row;
-    if (m >= A.M) continue;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sum[w][token][row];
-    out[token * ldo + m] = from_float<T>(v);
+__global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kernel(const ExpertParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  griddep_wait();
+  griddep_launch_dependents();
+  if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
+  const Slot slot = p.ws.slots[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t pair0 = blockIdx.x * p.pairs;
+  const int32_t strip = min(2 * (pair0 + warp % p.pairs), p.down.strips - 1);
+  const StripAt at[2] = {StripAt(p.down, p.down.unit(slot.expert, strip, 0), lane),
+                         StripAt(p.down, p.down.unit(slot.expert, min(strip + 1, p.down.strips - 1), 0), lane)};
+  for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
+    const int32_t rows = min(slot.count - n0, NT * 8), first = slot.first + n0;
+    float acc[2][NT][4] = {};
+    strip_product<T, NG, NT>(
+        at, p.down.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, p.shared,
+        [&](int32_t n) { return p.ws.h + (first + n) * p.ws.ldh; }, acc);
+    strip_reduce<NT, false>(acc, p.pairs, rows, smem, [&](int pair, int32_t n, int32_t row, float sum, float) {
+      const int64_t m = static_cast<int64_t>(pair0 + pair) * 32 + row;
+      if (m < p.down.M) p.ws.y[static_cast<int64_t>(first + n) * p.down.M + m] = p.ws.pair_weight[first + n] * sum;
+    });
   }
 }
 
+// out[token] = the sum of its pairs' y, in the order of its choice.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_join_kernel(const float* __restrict__ y, const int32_t* __restrict__ place,
+                                                       int32_t top_k, int32_t H, T* __restrict__ out, int64_t ldo) {
+  __shared__ int32_t at[kMoeMaxTopK];
+  griddep_wait();
+  if (threadIdx.x < top_k) at[threadIdx.x] = place[blockIdx.y * top_k + threadIdx.x];
+  __syncthreads();
+  const int32_t m = blockIdx.x * 256 + threadIdx.x;
+  if (m >= H) return;
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int32_t j = 0; j < top_k; ++j)
+    if (at[j] >= 0) sum += y[static_cast<int64_t>(at[j]) * H + m];
+  out[blockIdx.y * ldo + m] = from_float<T>(sum);
+}
+
+// ---------------------------------------------------------------- host
+
+// A kernel that may start while the one before it in the stream ends.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, int cluster, cudaStream_t s,
+                         Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 template <typename T, int NG, int NT>
-void experts_as(const MoeCall& p, const uint16_t* X, int64_t ldx, int32_t H, const Workspace& ws,
-                cudaStream_t s) {
-  const W4Dev gate = w4_dev(&p.gate), down = w4_dev(&p.down);
-  const int64_t most = min64(p.gate.count, static_cast<int64_t>(p.tokens) * p.top_k);
-  const dim3 grid(gate.strips, static_cast<unsigned>(most));
-  if (p.up.codes)
-    moe_gate_up_kernel<T, NG, 2, NT>
-        <<<grid, kWarps * 32, 0, s>>>(gate, w4_dev(&p.up), X, ldx, H, p.activation, ws);
+cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
+  auto gate_up = moe_gate_up_kernel<T, NG, NT>;
+  auto down = moe_down_kernel<T, NG, NT>;
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernels may use their shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(allowed.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(uint64_t(1) << (dev & 63));
+  }
+  const int64_t most = min64(c.gate.count, static_cast<int64_t>(c.tokens) * c.top_k);
+  const int32_t rows = c.tokens < NT * 8 ? c.tokens : NT * 8;
+  p.pairs = pairs_per_cta(most, p.gate.strips);
+  p.shared = strip_shared(rows, p.gate.units, NT);
+  e = launch_after(gate_up, dim3((p.gate.strips + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads,
+                   p.shared, 1, s, p);
+  if (e != cudaSuccess) return e;
+  const int32_t pairs = (p.down.strips + 1) / 2;
+  p.pairs = pairs_per_cta(most, pairs);
+  p.shared = strip_shared(rows, p.down.units, NT);
+  e = launch_after(down, dim3((pairs + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
+                   1, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_after(moe_join_kernel<T>, dim3((p.down.M + 255) / 256, c.tokens), 256, 0, 1, s,
+                      static_cast<const float*>(p.ws.y), static_cast<const int32_t*>(p.ws.place), c.top_k, p.down.M,
+                      static_cast<T*>(c.out), c.ldo);
+}
+
+template <typename T, typename RT>
+cudaError_t logits_as(const MoeCall& c, const ExpertParams& p, cudaStream_t s) {
+  const int32_t H = c.gate.K, E = c.gate.count;
+  const bool vec = (reinterpret_cast<uintptr_t>(c.router) & 15u) == 0 && H % 8 == 0;
+#define FLASHSPMM_LOGITS(VEC, EB, TB)                                                                       \
+  moe_logits_kernel<T, RT, VEC, EB, TB><<<dim3((E + EB - 1) / EB, (c.tokens + TB - 1) / TB), 256, 0, s>>>( \
+      p.X, p.ldx, c.router, H, c.tokens, E, p.ws.logits)
+  if (c.tokens == 1)
+    vec ? FLASHSPMM_LOGITS(true, 1, 1) : FLASHSPMM_LOGITS(false, 1, 1);
   else
-    moe_gate_up_kernel<T, NG, 1, NT><<<grid, kWarps * 32, 0, s>>>(gate, gate, X, ldx, H, p.activation, ws);
+    vec ? FLASHSPMM_LOGITS(true, 2, 4) : FLASHSPMM_LOGITS(false, 2, 4);
+#undef FLASHSPMM_LOGITS
   note_launch();
-  moe_down_kernel<T, NG, NT>
-      <<<down.strips, kWarps * 32, 0, s>>>(down, p.tokens, static_cast<T*>(p.out), p.ldo, ws);
-  note_launch();
+  return cudaGetLastError();
 }
 
 template <typename T>
-void layer_as(const MoeCall& p, const Workspace& ws, const uint16_t* X, int64_t ldx, cudaStream_t s) {
-  const int32_t H = p.gate.K, E = p.gate.count;
-  // X is aligned and padded here, so its rows can be read to a multiple of 8
-  const int32_t Hp = static_cast<int32_t>(aligned_k(H));
-  if (p.router) {
-    const dim3 grid((E + kWarps - 1) / kWarps, (p.tokens + 3) / 4);
-    const bool vec = (reinterpret_cast<uintptr_t>(p.router) & 15u) == 0 && H % 8 == 0;
-#define FLASHSPMM_LOGITS(RT, VEC) \
-  moe_logits_kernel<T, RT, VEC><<<grid, kWarps * 32, 0, s>>>(X, ldx, p.router, H, p.tokens, E, ws.logits)
-    if (p.router_dtype == FLASHSPMM_F32)
-      vec ? FLASHSPMM_LOGITS(float, true) : FLASHSPMM_LOGITS(float, false);
-    else
-      vec ? FLASHSPMM_LOGITS(T, true) : FLASHSPMM_LOGITS(T, false);
-#undef FLASHSPMM_LOGITS
-    note_launch();
-  }
-  moe_route_kernel<<<1, kRouteThreads, 0, s>>>(p.router == nullptr, p.tokens, E, p.top_k, p.renormalize,
-                                               p.ids, p.weights, ws);
-  note_launch();
-#define FLASHSPMM_EXPERTS(NG)                       \
-  if (p.tokens <= 8)                               \
-    experts_as<T, NG, 1>(p, X, ldx, Hp, ws, s);     \
-  else if (p.tokens <= 16)                         \
-    experts_as<T, NG, 2>(p, X, ldx, Hp, ws, s);     \
-  else if (p.tokens <= 32)                         \
-    experts_as<T, NG, 4>(p, X, ldx, Hp, ws, s);     \
-  else                                              \
-    experts_as<T, NG, 8>(p, X, ldx, Hp, ws, s)
-  if (p.gate.group == 128) {
-    FLASHSPMM_EXPERTS(1);
-  } else if (p.gate.group == 64) {
-    FLASHSPMM_EXPERTS(2);
-  } else {
-    FLASHSPMM_EXPERTS(4);
-  }
+cudaError_t layer_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
+  const int32_t E = c.gate.count;
+  cudaError_t e = cudaSuccess;
+  if (c.router) e = c.router_dtype == FLASHSPMM_F32 ? logits_as<T, float>(c, p, s) : logits_as<T, T>(c, p, s);
+  if (e != cudaSuccess) return e;
+  auto route = E <= 64 ? moe_route_kernel<2> : E <= 128 ? moe_route_kernel<4> : moe_route_kernel<16>;
+  e = launch_after(route, dim3(kRouteCtas), kRouteThreads, 0, kRouteCtas, s, c.router == nullptr, c.tokens, E, c.top_k,
+                   c.renormalize, c.ids, c.weights, p.ws);
+  if (e != cudaSuccess) return e;
+  // Tokens that an expert's codes serve at a time: 8, 16 or 32.  An expert with more reads its codes again, so
+  // 32, which leave an SM half as many warps, are for experts that get more than 12 on average.
+  const bool many = static_cast<int64_t>(c.tokens) * c.top_k > 12 * static_cast<int64_t>(E);
+#define FLASHSPMM_EXPERTS(NG)                                  \
+  c.tokens <= 8             ? experts_as<T, NG, 1>(c, p, s)    \
+  : c.tokens <= 16 || !many ? experts_as<T, NG, 2>(c, p, s)    \
+                            : experts_as<T, NG, 4>(c, p, s)
+  return c.gate.group == 128  ? FLASHSPMM_EXPERTS(1)
+         : c.gate.group == 64 ? FLASHSPMM_EXPERTS(2)
+                              : FLASHSPMM_EXPERTS(4);
 #undef FLASHSPMM_EXPERTS
 }
 
@@ -463,23 +522,25 @@ size_t moe_workspace(int32_t T, int32_t E, int32_t top_k, int32_t H, int32_t F, 
   return carve(nullptr, T, E, top_k, H, F, aligned).bytes;
 }
 
-cudaError_t launch_moe_w4(const MoeCall& p, void* workspace, cudaStream_t s) {
-  const int32_t H = p.gate.K;
-  const bool aligned = rows_aligned(p.X, p.ldx, H);
-  const Workspace ws = carve(workspace, p.tokens, p.gate.count, p.top_k, H, p.gate.M, aligned);
-  const uint16_t* X = static_cast<const uint16_t*>(p.X);
-  int64_t ldx = p.ldx;
+cudaError_t launch_moe_w4(const MoeCall& c, void* workspace, cudaStream_t s) {
+  const int32_t H = c.gate.K;
+  const bool aligned = rows_aligned(c.X, c.ldx, H);
+  ExpertParams p{};
+  p.ws = carve(workspace, c.tokens, c.gate.count, c.top_k, H, c.gate.M, aligned);
+  p.gate = w4_dev(&c.gate);
+  if (c.up.codes) p.up = w4_dev(&c.up);
+  p.down = w4_dev(&c.down);
+  p.X = static_cast<const uint16_t*>(c.X);
+  p.ldx = c.ldx;
+  p.H = static_cast<int32_t>(aligned_k(H));  // the aligned copy is padded with zeros
+  p.activation = c.activation;
   if (!aligned) {
-    const cudaError_t e = launch_align_rows(p.X, p.ldx, p.tokens, H, ws.x, s);
+    const cudaError_t e = launch_align_rows(c.X, c.ldx, c.tokens, H, p.ws.x, s);
     if (e != cudaSuccess) return e;
-    X = ws.x;
-    ldx = aligned_k(H);
+    p.X = p.ws.x;
+    p.ldx = aligned_k(H);
   }
-  if (p.gate.dtype == FLASHSPMM_F16)
-    layer_as<__half>(p, ws, X, ldx, s);
-  else
-    layer_as<__nv_bfloat16>(p, ws, X, ldx, s);
-  return cudaGetLastError();
+  return c.gate.dtype == FLASHSPMM_F16 ? layer_as<__half>(c, p, s) : layer_as<__nv_bfloat16>(c, p, s);
 }
 
 }  // namespace flashspmm

@@ -219,8 +219,8 @@ __device__ __forceinline__ uint4 load_act8(const uint16_t* row, int32_t k, int32
 // Scales and zero points of one unit as a lane needs them (NG groups a unit).
 template <typename T, int NG>
 struct W4Groups {
-  uint32_t s[NG];  // {row g, row g + 8} in 16 bits each
-  uint32_t z[NG];  // {row g, row g + 8} in 8 bits each
+  uint32_t s[NG];            // {row g, row g + 8} in 16 bits each
+  uint32_t z[(NG + 1) / 2];  // {row g, row g + 8} in 8 bits each, two groups to a word
 
   __device__ __forceinline__ void load(const W4Dev& A, int64_t unit, int g) {
     const int64_t at = (unit * 8 + g) * (NG * 2);
@@ -229,41 +229,28 @@ struct W4Groups {
   __device__ __forceinline__ void load(const uint16_t* sp, const uint8_t* zp) {
     if (NG == 1) {
       s[0] = *reinterpret_cast<const uint32_t*>(sp);
+      z[0] = zp ? *reinterpret_cast<const uint16_t*>(zp) : 0x0808u;
     } else if (NG == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(sp);
       s[0] = v.x;
       s[NG - 1] = v.y;
+      z[0] = zp ? *reinterpret_cast<const uint32_t*>(zp) : 0x08080808u;
     } else {
       const uint4 v = *reinterpret_cast<const uint4*>(sp);
       s[0] = v.x;
       s[1 % NG] = v.y;
       s[2 % NG] = v.z;
       s[NG - 1] = v.w;
-    }
-    if (zp) {
-      if (NG == 1) {
-        z[0] = *reinterpret_cast<const uint16_t*>(zp);
-      } else if (NG == 2) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(zp);
-        z[0] = v & 0xFFFF;
-        z[NG - 1] = v >> 16;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(zp);
-        z[0] = v.x & 0xFFFF;
-        z[1 % NG] = v.x >> 16;
-        z[2 % NG] = v.y & 0xFFFF;
-        z[NG - 1] = v.y >> 16;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NG; ++i) z[i] = 0x0808u;
+      const uint2 q = zp ? *reinterpret_cast<const uint2*>(zp) : make_uint2(0x08080808u, 0x08080808u);
+      z[0] = q.x;
+      z[(NG - 1) / 2] = q.y;
     }
   }
   __device__ __forceinline__ float scale(int i, int row) const {
     return bits_to_float<T>(static_cast<uint16_t>(row ? s[i] >> 16 : s[i] & 0xFFFF));
   }
   __device__ __forceinline__ int zero_point(int i, int row) const {
-    return static_cast<int>(row ? z[i] >> 8 : z[i] & 0xFF);
+    return static_cast<int>(z[i >> 1] >> (16 * (i & 1) + 8 * row) & 0xFF);
   }
   __device__ __forceinline__ W4Zero<T> zero(int i) const { return W4Zero<T>(zero_point(i, 0), zero_point(i, 1)); }
 };

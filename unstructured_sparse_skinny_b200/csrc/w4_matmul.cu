@@ -1,73 +1,63 @@
 // Skinny product with 4-bit weights: C[N][M] = B[N][K] x A[M][K]^T, N <= 256.
-//
-// A CTA owns R strips of 16 rows and NT tiles of 8 activation rows; its warps
-// share the units of 128 columns and the CTA adds their sums in a fixed order.
-#include "w4.cuh"
+// Few tokens run on the strips' engine (w4_strips.cuh), more on tcgen05
+// (w4_gemm.cu).
+#include <atomic>
+
+#include "w4_strips.cuh"
 
 namespace flashspmm {
 namespace {
 
-constexpr int kWarps = 8;
+struct MatmulParams {
+  W4Dev A;
+  const uint16_t* B;
+  int64_t ldb;
+  void* C;
+  int64_t ldc;
+  bool c_f32;
+  int32_t N;
+  int32_t pairs;  // of strips a CTA
+  uint32_t shared;
+};
 
-template <typename T, int NG, int R, int NT>
-__global__ void __launch_bounds__(kWarps * 32) w4_matmul_kernel(W4Dev A, const uint16_t* __restrict__ B, int64_t ldb,
-                                                                void* C, int64_t ldc, bool c_f32, int32_t N) {
-  constexpr int kRows = 16 * R, kPitch = kRows + 4;  // + 4: the lanes of a fragment store to 32 banks
-  __shared__ float red[kWarps][NT * 8][kPitch];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int32_t n0 = blockIdx.y * (NT * 8);
-  const int32_t strip0 = blockIdx.x * R;
-  const int tiles = min(NT, (N - n0 + 7) / 8);
-  float acc[R][NT][4] = {};
-  const auto act = [&](int nt, int32_t k) {
-    const int32_t n = n0 + 8 * nt + g;
-    return load_act8<true>(n < N ? B + n * ldb : nullptr, k + 8 * t, A.K);
-  };
-  for (int32_t u = warp; u < A.units; u += kWarps) {
-    uint4 c[R][2];
-    W4Groups<T, NG> grp[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t unit = A.unit(0, min(strip0 + r, A.strips - 1), u);
-      c[r][0] = ld_stream(A.codes + unit * 64 + lane);
-      c[r][1] = ld_stream(A.codes + unit * 64 + 32 + lane);
-      grp[r].load(A, unit, g);
-    }
-    w4_unit<T, NG, R, NT>(c, grp, u * kW4UnitCols, tiles, act, acc);
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][nt * 8 + 2 * t + (i & 1)][r * 16 + g + 8 * (i >> 1)] = acc[r][nt][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < NT * 8 * kRows; i += kWarps * 32) {
-    const int n = i / kRows, row = i - n * kRows;
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += red[w][n][row];
-    const int64_t m = static_cast<int64_t>(strip0) * 16 + row;
-    if (n0 + n < N && m < A.M) {
-      if (c_f32)
-        static_cast<float*>(C)[(n0 + n) * ldc + m] = sum;
-      else
-        static_cast<T*>(C)[(n0 + n) * ldc + m] = from_float<T>(sum);
-    }
-  }
+template <typename T, int NG, int NT>
+__global__ void __launch_bounds__(kStripThreads, 2) w4_matmul_kernel(const MatmulParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t pair0 = blockIdx.x * p.pairs;
+  const int32_t strip = min(2 * (pair0 + warp % p.pairs), p.A.strips - 1);
+  const StripAt at[2] = {StripAt(p.A, p.A.unit(0, strip, 0), lane),
+                         StripAt(p.A, p.A.unit(0, min(strip + 1, p.A.strips - 1), 0), lane)};
+  float acc[2][NT][4] = {};
+  strip_product<T, NG, NT>(
+      at, p.A.units, p.A.K, p.N, p.pairs, smem, p.shared, [&](int32_t n) { return p.B + n * p.ldb; }, acc);
+  strip_reduce<NT, false>(acc, p.pairs, p.N, smem, [&](int pair, int32_t n, int32_t row, float sum, float) {
+    const int64_t m = static_cast<int64_t>(pair0 + pair) * 32 + row;
+    if (m >= p.A.M) return;
+    if (p.c_f32)
+      static_cast<float*>(p.C)[n * p.ldc + m] = sum;
+    else
+      static_cast<T*>(p.C)[n * p.ldc + m] = from_float<T>(sum);
+  });
 }
 
-template <typename T, int NG>
-void matmul_as(const W4Dev& A, const uint16_t* B, int64_t ldb, void* C, int64_t ldc, bool c_f32, int32_t N,
-               cudaStream_t s) {
-#define FLASHSPMM_MATMUL(R, NT)                                                                                     \
-  w4_matmul_kernel<T, NG, R, NT><<<dim3((A.strips + R - 1) / R, (N + NT * 8 - 1) / (NT * 8)), kWarps * 32, 0, s>>>( \
-      A, B, ldb, C, ldc, c_f32, N)
-  if (N <= 8)
-    FLASHSPMM_MATMUL(2, 1);
-  else
-    FLASHSPMM_MATMUL(2, 2);
-#undef FLASHSPMM_MATMUL
+template <typename T, int NG, int NT>
+cudaError_t launch_as(MatmulParams& p, cudaStream_t s) {
+  auto kernel = w4_matmul_kernel<T, NG, NT>;
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(allowed.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(uint64_t(1) << (dev & 63));
+  }
+  const int32_t pairs = (p.A.strips + 1) / 2;
+  p.pairs = pairs_per_cta(1, pairs);
+  p.shared = strip_shared(p.N, p.A.units, NT);
+  kernel<<<(pairs + p.pairs - 1) / p.pairs, kStripThreads, p.shared, s>>>(p);
+  return cudaGetLastError();
 }
 
 __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* __restrict__ X, int64_t ld, int32_t K,
@@ -100,30 +90,35 @@ size_t w4_matmul_workspace(int32_t M, int32_t K, int32_t N, bool aligned) {
 cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                              int32_t N, void* workspace, cudaStream_t s) {
   if (N > kW4FragmentTokens) return launch_w4_gemm(in, B, ldb, C, ldc, c_f32, N, workspace, s);
-  W4Dev A = w4_dev(in);
-  if (!rows_aligned(B, ldb, A.K)) {
-    const cudaError_t e = launch_align_rows(B, ldb, N, A.K, workspace, s);
+  MatmulParams p{};
+  p.A = w4_dev(in);
+  if (!rows_aligned(B, ldb, p.A.K)) {
+    const cudaError_t e = launch_align_rows(B, ldb, N, p.A.K, workspace, s);
     if (e != cudaSuccess) return e;
     B = workspace;
-    ldb = aligned_k(A.K);
-    A.K = static_cast<int32_t>(min64(ldb, INT32_MAX));
+    ldb = aligned_k(p.A.K);
+    p.A.K = static_cast<int32_t>(ldb);
   }
-  const uint16_t* b = static_cast<const uint16_t*>(B);
-#define FLASHSPMM_BY_GROUP(T)                                \
-  if (A.group == 128)                                        \
-    matmul_as<T, 1>(A, b, ldb, C, ldc, c_f32, N, s);         \
-  else if (A.group == 64)                                    \
-    matmul_as<T, 2>(A, b, ldb, C, ldc, c_f32, N, s);         \
-  else                                                       \
-    matmul_as<T, 4>(A, b, ldb, C, ldc, c_f32, N, s)
-  if (in->dtype == FLASHSPMM_F16) {
+  p.B = static_cast<const uint16_t*>(B);
+  p.ldb = ldb;
+  p.C = C;
+  p.ldc = ldc;
+  p.c_f32 = c_f32;
+  p.N = N;
+  cudaError_t e;
+#define FLASHSPMM_BY_TILES(T, NG) (N <= 8 ? launch_as<T, NG, 1>(p, s) : launch_as<T, NG, 2>(p, s))
+#define FLASHSPMM_BY_GROUP(T)                          \
+  e = p.A.group == 128  ? FLASHSPMM_BY_TILES(T, 1)     \
+      : p.A.group == 64 ? FLASHSPMM_BY_TILES(T, 2)     \
+                        : FLASHSPMM_BY_TILES(T, 4)
+  if (in->dtype == FLASHSPMM_F16)
     FLASHSPMM_BY_GROUP(__half);
-  } else {
+  else
     FLASHSPMM_BY_GROUP(__nv_bfloat16);
-  }
 #undef FLASHSPMM_BY_GROUP
+#undef FLASHSPMM_BY_TILES
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace flashspmm

@@ -414,7 +414,9 @@ flashspmm_status flashspmm_w4_decode(const flashspmm_w4* A, void* W, int32_t w_d
  * current device; 0 when none. */
 size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B, int64_t ldb, int32_t N);
 
-/* Skinny product C = A x B with fp32 sums.
+/* Skinny product C = A x B with fp32 sums.  Up to N = 8 the sums are of s times
+ * whole numbers q - z; above, a weight s * (q - z) is rounded to A->dtype first,
+ * as flashspmm_w4_decode gives it.
  *   A          a view with count = 1.
  *   B          device, A->dtype, N rows of K activations, ldb values apart
  *              (any alignment; rows that start on 16 bytes with K % 8 == 0 are

@@ -323,7 +323,7 @@ cudaError_t launch_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, 
                              int32_t N, void* workspace, cudaStream_t s);
 
 // The same product by tcgen05 (w4_gemm.cu), for N > kW4FragmentTokens.
-constexpr int kW4FragmentTokens = 16;
+constexpr int kW4FragmentTokens = 8;
 size_t w4_gemm_workspace(int32_t M, int32_t K, int32_t N);
 cudaError_t launch_w4_gemm(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                            int32_t N, void* workspace, cudaStream_t s);

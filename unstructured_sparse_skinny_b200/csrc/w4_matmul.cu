@@ -1,7 +1,5 @@
 // Skinny product with 4-bit weights: C[N][M] = B[N][K] x A[M][K]^T, N <= 256.
-// Few tokens run on the strips' engine (w4_strips.cuh), more on tcgen05
-// (w4_gemm.cu).
-#include <atomic>
+// Up to eight tokens run here, more on tcgen05 (w4_gemm.cu).
 
 #include "w4_strips.cuh"
 
@@ -16,48 +14,78 @@ struct MatmulParams {
   int64_t ldc;
   bool c_f32;
   int32_t N;
-  int32_t pairs;  // of strips a CTA
-  uint32_t shared;
 };
 
-template <typename T, int NG, int NT>
-__global__ void __launch_bounds__(kStripThreads, 2) w4_matmul_kernel(const MatmulParams p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t pair0 = blockIdx.x * p.pairs;
-  const int32_t strip = min(2 * (pair0 + warp % p.pairs), p.A.strips - 1);
-  const StripAt at[2] = {StripAt(p.A, p.A.unit(0, strip, 0), lane),
-                         StripAt(p.A, p.A.unit(0, min(strip + 1, p.A.strips - 1), 0), lane)};
-  float acc[2][NT][4] = {};
-  strip_product<T, NG, NT>(
-      at, p.A.units, p.A.K, p.N, p.pairs, smem, p.shared, [&](int32_t n) { return p.B + n * p.ldb; }, acc);
-  strip_reduce<NT, false>(acc, p.pairs, p.N, smem, [&](int pair, int32_t n, int32_t row, float sum, float) {
-    const int64_t m = static_cast<int64_t>(pair0 + pair) * 32 + row;
-    if (m >= p.A.M) return;
-    if (p.c_f32)
-      static_cast<float*>(p.C)[n * p.ldc + m] = sum;
-    else
-      static_cast<T*>(p.C)[n * p.ldc + m] = from_float<T>(sum);
-  });
-}
-
-template <typename T, int NG, int NT>
-cudaError_t launch_as(MatmulParams& p, cudaStream_t s) {
-  auto kernel = w4_matmul_kernel<T, NG, NT>;
-  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (!(allowed.load() >> (dev & 63) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
-    if (e != cudaSuccess) return e;
-    allowed.fetch_or(uint64_t(1) << (dev & 63));
+// One strip of 16 rows a CTA, up to eight tokens: its warps have the units in
+// turn and add up at the end.  Codes come two units ahead; the activations,
+// which all CTAs read again, from L1 and L2 as the fragments need them.  (Staged
+// in shared memory first, they delay the short-lived CTAs more than they save:
+// 29 and 54 us for one and eight tokens of 12288^2.)
+template <typename T, int NG>
+__global__ void __launch_bounds__(kStripThreads, 4) w4_matmul_kernel(const MatmulParams p) {
+  constexpr int kAhead = 2, kBlocks = 4 / NG;
+  __shared__ float red[kStripWarps][8][20];  // 16 rows, and the fragments' stores meet all banks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const StripAt at(p.A, p.A.unit(0, blockIdx.x, 0), lane);
+  const int32_t units = p.A.units;
+  const uint16_t* row = g < p.N ? p.B + g * p.ldb + 8 * t : nullptr;
+  StripUnit<T, NG> buf[kAhead];
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d)
+    if (warp + d * kStripWarps < units) buf[d].load(at, warp + d * kStripWarps);
+  float acc[4] = {};
+  for (int32_t base = warp; base < units; base += kAhead * kStripWarps) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int32_t u = base + d * kStripWarps;
+      if (u >= units) break;
+      uint4 x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        x[b] = make_uint4(0, 0, 0, 0);
+        if (row && u * 128 + 32 * b + 8 * t < p.A.K) x[b] = __ldg(reinterpret_cast<const uint4*>(row + u * 128 + 32 * b));
+      }
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) {
+        const W4Zero<T> z = buf[d].g.zero(gi);
+        float sum[4];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          const int blk = gi * kBlocks + b;
+          uint32_t a[2][4];
+          w4_fragment(buf[d].word(2 * blk), z, a[0]);
+          w4_fragment(buf[d].word(2 * blk + 1), z, a[1]);
+          if (b == 0)
+            mma16816_zero<T>(sum, a[0], x[blk].x, x[blk].y);
+          else
+            mma16816<T>(sum, a[0], x[blk].x, x[blk].y);
+          mma16816<T>(sum, a[1], x[blk].z, x[blk].w);
+        }
+        const float s0 = buf[d].g.scale(gi, 0), s1 = buf[d].g.scale(gi, 1);
+        acc[0] = fmaf(s0, sum[0], acc[0]);
+        acc[1] = fmaf(s0, sum[1], acc[1]);
+        acc[2] = fmaf(s1, sum[2], acc[2]);
+        acc[3] = fmaf(s1, sum[3], acc[3]);
+      }
+      if (u + kAhead * kStripWarps < units) buf[d].load(at, u + kAhead * kStripWarps);
+    }
   }
-  const int32_t pairs = (p.A.strips + 1) / 2;
-  p.pairs = pairs_per_cta(1, pairs);
-  p.shared = strip_shared(p.N, p.A.units, NT);
-  kernel<<<(pairs + p.pairs - 1) / p.pairs, kStripThreads, p.shared, s>>>(p);
-  return cudaGetLastError();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[i];
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int n = threadIdx.x >> 4, r = threadIdx.x & 15;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kStripWarps; ++w) sum += red[w][n][r];
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + r;
+    if (n < p.N && m < p.A.M) {
+      if (p.c_f32)
+        static_cast<float*>(p.C)[n * p.ldc + m] = sum;
+      else
+        static_cast<T*>(p.C)[n * p.ldc + m] = from_float<T>(sum);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* __restrict__ X, int64_t ld, int32_t K,
@@ -105,20 +133,17 @@ cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb,
   p.ldc = ldc;
   p.c_f32 = c_f32;
   p.N = N;
-  cudaError_t e;
-#define FLASHSPMM_BY_TILES(T, NG) (N <= 8 ? launch_as<T, NG, 1>(p, s) : launch_as<T, NG, 2>(p, s))
-#define FLASHSPMM_BY_GROUP(T)                          \
-  e = p.A.group == 128  ? FLASHSPMM_BY_TILES(T, 1)     \
-      : p.A.group == 64 ? FLASHSPMM_BY_TILES(T, 2)     \
-                        : FLASHSPMM_BY_TILES(T, 4)
+#define FLASHSPMM_BY_GROUP(T)                                                                \
+  p.A.group == 128  ? w4_matmul_kernel<T, 1><<<p.A.strips, kStripThreads, 0, s>>>(p)         \
+  : p.A.group == 64 ? w4_matmul_kernel<T, 2><<<p.A.strips, kStripThreads, 0, s>>>(p)         \
+                    : w4_matmul_kernel<T, 4><<<p.A.strips, kStripThreads, 0, s>>>(p)
   if (in->dtype == FLASHSPMM_F16)
     FLASHSPMM_BY_GROUP(__half);
   else
     FLASHSPMM_BY_GROUP(__nv_bfloat16);
 #undef FLASHSPMM_BY_GROUP
-#undef FLASHSPMM_BY_TILES
   note_launch();
-  return e;
+  return cudaGetLastError();
 }
 
 }  // namespace flashspmm

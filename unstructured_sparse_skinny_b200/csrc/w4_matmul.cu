@@ -6,6 +6,8 @@
 namespace flashspmm {
 namespace {
 
+constexpr int kMatmulWarps = 12;
+
 struct MatmulParams {
   W4Dev A;
   const uint16_t* B;
@@ -22,9 +24,9 @@ struct MatmulParams {
 // in shared memory first, they delay the short-lived CTAs more than they save:
 // 29 and 54 us for one and eight tokens of 12288^2.)
 template <typename T, int NG>
-__global__ void __launch_bounds__(kStripThreads, 4) w4_matmul_kernel(const MatmulParams p) {
+__global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const MatmulParams p) {
   constexpr int kAhead = 2, kBlocks = 4 / NG;
-  __shared__ float red[kStripWarps][8][20];  // 16 rows, and the fragments' stores meet all banks
+  __shared__ float red[kMatmulWarps][8][20];  // 16 rows, and the fragments' stores meet all banks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const StripAt at(p.A, p.A.unit(0, blockIdx.x, 0), lane);
   const int32_t units = p.A.units;
@@ -32,12 +34,12 @@ __global__ void __launch_bounds__(kStripThreads, 4) w4_matmul_kernel(const Matmu
   StripUnit<T, NG> buf[kAhead];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
-    if (warp + d * kStripWarps < units) buf[d].load(at, warp + d * kStripWarps);
+    if (warp + d * kMatmulWarps < units) buf[d].load(at, warp + d * kMatmulWarps);
   float acc[4] = {};
-  for (int32_t base = warp; base < units; base += kAhead * kStripWarps) {
+  for (int32_t base = warp; base < units; base += kAhead * kMatmulWarps) {
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
-      const int32_t u = base + d * kStripWarps;
+      const int32_t u = base + d * kMatmulWarps;
       if (u >= units) break;
       uint4 x[4];
 #pragma unroll
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kStripThreads, 4) w4_matmul_kernel(const Matmu
         acc[2] = fmaf(s1, sum[2], acc[2]);
         acc[3] = fmaf(s1, sum[3], acc[3]);
       }
-      if (u + kAhead * kStripWarps < units) buf[d].load(at, u + kAhead * kStripWarps);
+      if (u + kAhead * kMatmulWarps < units) buf[d].load(at, u + kAhead * kMatmulWarps);
     }
   }
 #pragma unroll
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kStripThreads, 4) w4_matmul_kernel(const Matmu
     const int n = threadIdx.x >> 4, r = threadIdx.x & 15;
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kStripWarps; ++w) sum += red[w][n][r];
+    for (int w = 0; w < kMatmulWarps; ++w) sum += red[w][n][r];
     const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + r;
     if (n < p.N && m < p.A.M) {
       if (p.c_f32)
@@ -134,9 +136,9 @@ cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb,
   p.c_f32 = c_f32;
   p.N = N;
 #define FLASHSPMM_BY_GROUP(T)                                                                \
-  p.A.group == 128  ? w4_matmul_kernel<T, 1><<<p.A.strips, kStripThreads, 0, s>>>(p)         \
-  : p.A.group == 64 ? w4_matmul_kernel<T, 2><<<p.A.strips, kStripThreads, 0, s>>>(p)         \
-                    : w4_matmul_kernel<T, 4><<<p.A.strips, kStripThreads, 0, s>>>(p)
+  p.A.group == 128  ? w4_matmul_kernel<T, 1><<<p.A.strips, kMatmulWarps * 32, 0, s>>>(p)         \
+  : p.A.group == 64 ? w4_matmul_kernel<T, 2><<<p.A.strips, kMatmulWarps * 32, 0, s>>>(p)         \
+                    : w4_matmul_kernel<T, 4><<<p.A.strips, kMatmulWarps * 32, 0, s>>>(p)
   if (in->dtype == FLASHSPMM_F16)
     FLASHSPMM_BY_GROUP(__half);
   else

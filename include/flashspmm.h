@@ -360,37 +360,35 @@ enum { FLASHSPMM_F16 = 0, FLASHSPMM_BF16 = 1, FLASHSPMM_F32 = 2 };
 enum { FLASHSPMM_ACT_SILU = 0, FLASHSPMM_ACT_GELU = 1, FLASHSPMM_ACT_RELU = 2 };
 
 /* A view of `count` 4-bit matrices of M x K one behind the other (1: a single
- * weight).  The buffers are the caller's, of flashspmm_w4_sizes bytes, written
- * by flashspmm_w4_encode or flashspmm_w4_pack.
+ * weight).  The data are the caller's, flashspmm_w4_bytes long, written by
+ * flashspmm_w4_encode or flashspmm_w4_pack.
  *
  * Layout: blocks of 128 rows (eight strips of 16) times units of 128 columns,
- * both padded with zero weights; the unit of one strip takes 1024 bytes of
- * codes at (((matrix * ceil(M/128) + block) * ceil(K/128) + unit) * 8 + strip)
- * * 1024, ordered so that lane 4 g + t of a warp finds the codes of its
- * tensor-core fragments (rows g and g + 8, columns 32 b + 8 t .. + 7 of each
- * 32-column block b) in two 16-byte loads.  Its scales and zero points are
- * [8][128 / group][2] entries: [g][group][row g, row g + 8]. */
+ * both padded with zero weights.  The unit of one strip is a record of 1024
+ * bytes of codes, 32 * (128 / group) bytes of scales and, with zero points,
+ * 16 * (128 / group) bytes of them; it is the (((matrix * ceil(M/128) + block) *
+ * ceil(K/128) + unit) * 8 + strip)-th record.  Codes are ordered so that lane
+ * 4 g + t of a warp finds those of its tensor-core fragments (rows g and g + 8,
+ * columns 32 b + 8 t .. + 7 of each 32-column block b) in two 16-byte loads.
+ * Scales and zero points are [8][128 / group][2] entries: [g][group][row g,
+ * row g + 8]. */
 typedef struct {
-  int32_t M, K;          /* rows and columns of one matrix, each <= 2^30 */
-  int32_t count;         /* matrices, >= 1 */
-  int32_t group;         /* columns that share a scale: 32, 64 or 128 */
-  int32_t dtype;         /* FLASHSPMM_F16 or FLASHSPMM_BF16: of the scales and of the activations they meet */
-  int32_t reserved;      /* must be 0 */
-  void* codes;           /* device, 16-byte aligned */
-  void* scales;          /* device, `dtype`, 16-byte aligned */
-  uint8_t* zeros;        /* device, 16-byte aligned; NULL: every zero point is 8 */
+  int32_t M, K;   /* rows and columns of one matrix, each <= 2^30 */
+  int32_t count;  /* matrices, >= 1 */
+  int32_t group;  /* columns that share a scale: 32, 64 or 128 */
+  int32_t dtype;  /* FLASHSPMM_F16 or FLASHSPMM_BF16: of the scales and of the activations they meet */
+  int32_t zeros;  /* 1: a zero point for each scale; 0: every zero point is 8 */
+  void* data;     /* device, 16-byte aligned */
 } flashspmm_w4;
 
-/* Bytes of codes and entries of scales and of zero points that a view of these
- * sizes holds.  Any output may be NULL.  0, or -1 on bad arguments. */
-int flashspmm_w4_sizes(int32_t M, int32_t K, int32_t count, int32_t group, int64_t* codes_bytes, int64_t* scales,
-                       int64_t* zeros);
+/* Bytes of data that a view of these sizes holds; -1 on bad arguments. */
+int64_t flashspmm_w4_bytes(int32_t M, int32_t K, int32_t count, int32_t group, int32_t zeros);
 
-/* Encoder: a dense weight to A's buffers.
+/* Encoder: a dense weight to A's data.
  *   W          device, A->dtype, count * M rows of K values, ldw values apart.
- *   symmetric  1: s = max|w| / 7, z = 8 (A->zeros must be NULL).
+ *   symmetric  1: s = max|w| / 7, z = 8 (A->zeros must be 0).
  *              0: s = (max(w, 0) - min(w, 0)) / 15, z = round(-min(w, 0) / s)
- *              clamped to 0..15 (A->zeros must be there).
+ *              clamped to 0..15 (A->zeros must be 1).
  * s is rounded to A->dtype and q = clamp(round(w / s) + z, 0, 15); roundings
  * are to nearest, ties to even.  A group whose s is zero has q = z.  A group
  * with a NaN or an infinity gets such a scale, so it decodes to values that
@@ -402,7 +400,7 @@ flashspmm_status flashspmm_w4_encode(const void* W, int64_t ldw, int32_t symmetr
  *   codes   device uint8[count * M][K], one code each, the low 4 bits are used.
  *   scales  device, A->dtype, [count * M][ceil(K / group)].
  *   zeros   device uint8 of the same shape, 0..63 (the low 6 bits are used);
- *           NULL if and only if A->zeros is NULL. */
+ *           NULL if and only if A->zeros is 0. */
 flashspmm_status flashspmm_w4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros,
                                    const flashspmm_w4* A, void* stream);
 

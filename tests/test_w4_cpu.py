@@ -22,33 +22,31 @@ def lib():
 
 
 def view(**kw):
-    v = dict(M=128, K=256, count=1, group=128, dtype=F16, reserved=0, codes=FAKE, scales=FAKE, zeros=None)
+    v = dict(M=128, K=256, count=1, group=128, dtype=F16, zeros=0, data=FAKE)
     v.update(kw)
     return _W4View(**v)
 
 
-@pytest.mark.parametrize("M,K,count,group,units", [
+@pytest.mark.parametrize("zeros", [0, 1])
+@pytest.mark.parametrize("M,K,count,group,records", [
     (16, 128, 1, 128, 8), (129, 129, 1, 64, 32), (1, 1, 3, 32, 24), (0, 128, 1, 128, 0),
-    (4099, 5003, 2, 32, 2 * 33 * 8 * 40),
-    (1 << 20, 1 << 20, 4, 128, 4 * (1 << 16) * (1 << 13)),
+    (4099, 5003, 2, 32, 2 * 33 * 8 * 40), (1 << 20, 1 << 20, 4, 128, 4 * (1 << 16) * (1 << 13)),
 ])
-def test_sizes(lib, M, K, count, group, units):
-    out = [ctypes.c_int64() for _ in range(3)]
-    assert lib.flashspmm_w4_sizes(M, K, count, group, *map(ctypes.byref, out)) == 0
-    groups = units * 16 * (128 // group)
-    assert [v.value for v in out] == [units * 1024, groups, groups]
+def test_bytes(lib, M, K, count, group, records, zeros):
+    groups = 16 * (128 // group)
+    assert lib.flashspmm_w4_bytes(M, K, count, group, zeros) == records * (1024 + groups * (3 if zeros else 2))
 
 
-@pytest.mark.parametrize("args", [(-1, 8, 1, 128), (8, -1, 1, 128), (8, 8, 0, 128), (8, 8, 1, 16), (8, 8, 1, 0),
-                                  (8, 8, 1, 256), ((1 << 30) + 1, 8, 1, 128)])
-def test_sizes_rejects(lib, args):
-    assert lib.flashspmm_w4_sizes(*args, None, None, None) == -1
+@pytest.mark.parametrize("args", [(-1, 8, 1, 128, 0), (8, -1, 1, 128, 0), (8, 8, 0, 128, 0), (8, 8, 1, 16, 0),
+                                  (8, 8, 1, 0, 0), (8, 8, 1, 256, 0), ((1 << 30) + 1, 8, 1, 128, 0),
+                                  (8, 8, 1, 128, 2), (8, 8, 1, 128, -1)])
+def test_bytes_rejects(lib, args):
+    assert lib.flashspmm_w4_bytes(*args) == -1
 
 
 BAD_VIEWS = [(dict(M=-1), INVALID), (dict(count=0), INVALID), (dict(group=96), UNSUPPORTED),
-             (dict(dtype=F32), UNSUPPORTED), (dict(reserved=1), INVALID), (dict(codes=None), INVALID),
-             (dict(scales=None), INVALID), (dict(codes=FAKE + 8), ALIGNMENT), (dict(scales=FAKE + 2), ALIGNMENT),
-             (dict(zeros=FAKE + 1), ALIGNMENT), (dict(K=(1 << 30) + 128), UNSUPPORTED)]
+             (dict(dtype=F32), UNSUPPORTED), (dict(zeros=2), INVALID), (dict(data=None), INVALID),
+             (dict(data=FAKE + 8), ALIGNMENT), (dict(K=(1 << 30) + 128), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,status", BAD_VIEWS)
@@ -70,11 +68,11 @@ def test_null_view(lib):
 
 
 @pytest.mark.parametrize("W,ldw,symmetric,zeros,status", [
-    (FAKE, 255, 1, None, INVALID),        # rows overlap
-    (FAKE, 256, 1, FAKE, INVALID),        # symmetric with zero points
-    (FAKE, 256, 0, None, INVALID),        # asymmetric without
-    (None, 256, 1, None, INVALID),
-    (FAKE + 1, 256, 1, None, ALIGNMENT),
+    (FAKE, 255, 1, 0, INVALID),        # rows overlap
+    (FAKE, 256, 1, 1, INVALID),        # symmetric with zero points
+    (FAKE, 256, 0, 0, INVALID),        # asymmetric without
+    (None, 256, 1, 0, INVALID),
+    (FAKE + 1, 256, 1, 0, ALIGNMENT),
 ])
 def test_encode_rejects(lib, W, ldw, symmetric, zeros, status):
     assert lib.flashspmm_w4_encode(W, ldw, symmetric, ctypes.byref(view(zeros=zeros)), None) == status
@@ -137,7 +135,7 @@ def test_moe_without_tokens_does_nothing(lib):
 
 def test_empty_matrices_do_nothing(lib):
     for kw in (dict(M=0), dict(K=0)):
-        v = ctypes.byref(view(codes=None, scales=None, **kw))
+        v = ctypes.byref(view(data=None, **kw))
         assert lib.flashspmm_w4_encode(None, 256, 1, v, None) == 0
         assert lib.flashspmm_w4_pack(None, None, None, v, None) == 0
         assert lib.flashspmm_w4_decode(v, None, F16, None) == 0

@@ -75,7 +75,7 @@ def load_library():
         "flashspmm_prefer_sparse": (ctypes.c_int, [I32, I32, I32, I64, I32]),
         "flashspmm_plan_owner": (ctypes.c_int64, [I32, I32, I32, I32, I32, ctypes.c_int64]),
         "flashspmm_plan_slot": (ctypes.c_int64, [I32, I32, I32, I32, I32, ctypes.c_int64, ctypes.c_int64]),
-        "flashspmm_w4_sizes": (ctypes.c_int, [I32, I32, I32, I32, P, P, P]),
+        "flashspmm_w4_bytes": (I64, [I32, I32, I32, I32, I32]),
         "flashspmm_w4_encode": (ctypes.c_int, [P, I64, I32, P, P]),
         "flashspmm_w4_pack": (ctypes.c_int, [P, P, P, P, P]),
         "flashspmm_w4_decode": (ctypes.c_int, [P, P, I32, P]),

@@ -334,20 +334,20 @@ __device__ __forceinline__ float activate(int kind, float v) {
 }
 
 struct ExpertParams {
-  W4Dev gate, up;        // up.codes null: no gate product
+  W4Dev gate, up;        // up.data null: no gate product
   W4Dev down;
   const uint16_t* X;
   int64_t ldx;
   int32_t H;             // columns of X that may be read
   int32_t activation;
-  int32_t pairs;         // of strips a CTA
+  int32_t slots;         // strips a CTA takes
   uint32_t shared;
   Workspace ws;
 };
 
 // h[pair][f] for some strips of 16 rows f of a running expert.  h is rounded
 // to the activations' type: it is the next product's tensor-core operand.
-template <typename T, int NG, int NT>
+template <typename T, int NG, int NT, bool Gated>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int32_t token[kMoeMaxTokens];
@@ -355,30 +355,29 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
   griddep_launch_dependents();
   if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
   const Slot slot = p.ws.slots[blockIdx.y];
-  const bool gated = p.up.codes != nullptr;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t strip0 = blockIdx.x * p.pairs;
-  const int64_t unit = p.gate.unit(slot.expert, min(strip0 + warp % p.pairs, p.gate.strips - 1), 0);
-  // without a gate product the second strip is the first again, and its sums are not used
-  const StripAt at[2] = {StripAt(p.gate, unit, lane), StripAt(gated ? p.up : p.gate, unit, lane)};
+  // with a gate product neighbouring warps have the same strip of gate and of up
+  const int w = (threadIdx.x >> 5) % p.slots;
+  const int32_t strip0 = blockIdx.x * (Gated ? p.slots / 2 : p.slots);
+  const W4Dev& A = Gated && (w & 1) ? p.up : p.gate;
+  const uint8_t* strip = A.at(A.unit(slot.expert, min(strip0 + (Gated ? w >> 1 : w), A.strips - 1), 0));
   if (threadIdx.x < slot.count) token[threadIdx.x] = p.ws.pair_token[slot.first + threadIdx.x];
   for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
     const int32_t rows = min(slot.count - n0, NT * 8);
-    float acc[2][NT][4] = {};
+    float acc[NT][4] = {};
     strip_product<T, NG, NT>(
-        at, p.gate.units, p.H, rows, p.pairs, smem, p.shared,
+        strip, 8 * A.record, A.zeros, A.units, p.H, rows, p.slots, smem, p.shared,
         [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
-    strip_reduce<NT, true>(acc, p.pairs, rows, smem, [&](int pair, int32_t n, int32_t row, float g, float u) {
-      const int32_t f = (strip0 + pair) * 16 + row;
+    strip_reduce<NT, Gated>(acc, p.slots, rows, smem, [&](int s, int32_t n, int32_t row, float g, float u) {
+      const int32_t f = (strip0 + s) * 16 + row;
       if (f >= p.ws.ldh) return;
-      const float v = activate(p.activation, g) * (gated ? u : 1.0f);
+      const float v = activate(p.activation, g) * (Gated ? u : 1.0f);
       // columns behind F pad h to 16 bytes: finite whatever x holds
       reinterpret_cast<T*>(p.ws.h)[(slot.first + n0 + n) * p.ws.ldh + f] = from_float<T>(f < p.gate.M ? v : 0.0f);
     });
   }
 }
 
-// y[pair] = weight * down h for some pairs of strips of a running expert.
+// y[pair] = weight * down h for some strips of a running expert.
 template <typename T, int NG, int NT>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -386,20 +385,19 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
   griddep_launch_dependents();
   if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
   const Slot slot = p.ws.slots[blockIdx.y];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t pair0 = blockIdx.x * p.pairs;
-  const int32_t strip = min(2 * (pair0 + warp % p.pairs), p.down.strips - 1);
-  const StripAt at[2] = {StripAt(p.down, p.down.unit(slot.expert, strip, 0), lane),
-                         StripAt(p.down, p.down.unit(slot.expert, min(strip + 1, p.down.strips - 1), 0), lane)};
+  const W4Dev& A = p.down;
+  const int32_t strip0 = blockIdx.x * p.slots;
+  const int w = (threadIdx.x >> 5) % p.slots;
+  const uint8_t* strip = A.at(A.unit(slot.expert, min(strip0 + w, A.strips - 1), 0));
   for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
     const int32_t rows = min(slot.count - n0, NT * 8), first = slot.first + n0;
-    float acc[2][NT][4] = {};
+    float acc[NT][4] = {};
     strip_product<T, NG, NT>(
-        at, p.down.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, p.shared,
+        strip, 8 * A.record, A.zeros, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.slots, smem, p.shared,
         [&](int32_t n) { return p.ws.h + (first + n) * p.ws.ldh; }, acc);
-    strip_reduce<NT, false>(acc, p.pairs, rows, smem, [&](int pair, int32_t n, int32_t row, float sum, float) {
-      const int64_t m = static_cast<int64_t>(pair0 + pair) * 32 + row;
-      if (m < p.down.M) p.ws.y[static_cast<int64_t>(first + n) * p.down.M + m] = p.ws.pair_weight[first + n] * sum;
+    strip_reduce<NT, false>(acc, p.slots, rows, smem, [&](int s, int32_t n, int32_t row, float sum, float) {
+      const int32_t m = (strip0 + s) * 16 + row;
+      if (m < A.M) p.ws.y[static_cast<int64_t>(first + n) * A.M + m] = p.ws.pair_weight[first + n] * sum;
     });
   }
 }
@@ -447,29 +445,31 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
 
 template <typename T, int NG, int NT>
 cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
-  auto gate_up = moe_gate_up_kernel<T, NG, NT>;
+  const bool gated = c.up.data != nullptr;
+  auto gate_up = gated ? moe_gate_up_kernel<T, NG, NT, true> : moe_gate_up_kernel<T, NG, NT, false>;
   auto down = moe_down_kernel<T, NG, NT>;
-  static std::atomic<uint64_t> allowed{0};  // devices on which the kernels may use their shared memory
+  static std::atomic<uint64_t> allowed[2];  // devices on which the kernels may use their shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (!(allowed.load() >> (dev & 63) & 1)) {
+  if (!(allowed[gated].load() >> (dev & 63) & 1)) {
     e = cudaFuncSetAttribute(gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
     if (e != cudaSuccess) return e;
-    allowed.fetch_or(uint64_t(1) << (dev & 63));
+    allowed[gated].fetch_or(uint64_t(1) << (dev & 63));
   }
   const int64_t most = min64(c.gate.count, static_cast<int64_t>(c.tokens) * c.top_k);
   const int32_t rows = c.tokens < NT * 8 ? c.tokens : NT * 8;
-  p.pairs = pairs_per_cta(most, p.gate.strips);
+  int32_t strips = p.gate.strips * (gated ? 2 : 1);
+  p.slots = strips_per_cta(most, strips, 2);
   p.shared = strip_shared(rows, p.gate.units, NT);
-  e = launch_after(gate_up, dim3((p.gate.strips + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads,
+  e = launch_after(gate_up, dim3((strips + p.slots - 1) / p.slots, static_cast<unsigned>(most)), kStripThreads,
                    p.shared, 1, s, p);
   if (e != cudaSuccess) return e;
-  const int32_t pairs = (p.down.strips + 1) / 2;
-  p.pairs = pairs_per_cta(most, pairs);
+  strips = p.down.strips;
+  p.slots = strips_per_cta(most, strips, 2);
   p.shared = strip_shared(rows, p.down.units, NT);
-  e = launch_after(down, dim3((pairs + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
+  e = launch_after(down, dim3((strips + p.slots - 1) / p.slots, static_cast<unsigned>(most)), kStripThreads, p.shared,
                    1, s, p);
   if (e != cudaSuccess) return e;
   return launch_after(moe_join_kernel<T>, dim3((p.down.M + 255) / 256, c.tokens), 256, 0, 1, s,
@@ -528,7 +528,7 @@ cudaError_t launch_moe_w4(const MoeCall& c, void* workspace, cudaStream_t s) {
   ExpertParams p{};
   p.ws = carve(workspace, c.tokens, c.gate.count, c.top_k, H, c.gate.M, aligned);
   p.gate = w4_dev(&c.gate);
-  if (c.up.codes) p.up = w4_dev(&c.up);
+  if (c.up.data) p.up = w4_dev(&c.up);
   p.down = w4_dev(&c.down);
   p.X = static_cast<const uint16_t*>(c.X);
   p.ldx = c.ldx;

@@ -2,10 +2,12 @@
 // product shared by the skinny matrix product and the experts' products.
 //
 // Layout.  A matrix of M x K codes is cut into strips of 16 rows, eight strips
-// to a block of 128, and units of 128 columns.  A unit of one strip takes 1024
-// bytes; the eight of a block follow one another, then come the block's next
-// 128 columns, so a block's unit is one copy for the large-batch kernel.  A
-// warp reads a unit of a strip with two 16-byte loads per lane, and every lane then holds
+// to a block of 128, and units of 128 columns.  A unit of one strip is one
+// record: 1024 bytes of codes, its scales and, if there are any, its zero
+// points.  The records of a block's eight strips follow one another, then come
+// the block's next 128 columns: a bulk copy costs the SM that issues it about
+// 100 ns whatever its size, so a block's unit, or some strips of it, is one
+// copy.  A warp reads a record's codes with two 16-byte loads per lane, and every lane then holds
 // exactly the codes of its own mma.m16n8k16 A fragments, so nothing is
 // shuffled or staged.  Lane l = 4 * g + t owns rows g and g + 8 and, in each
 // 32-column block b of the unit, the eight columns 32 * b + 8 * t .. + 7.  The
@@ -19,8 +21,8 @@
 // value of fragment register a_i (a0: row g, first pair; a1: row g + 8, first;
 // a2: row g, second; a3: row g + 8, second).
 //
-// Scales (16 bits) and zero points (8 bits) of a unit are [g][group][row g,
-// row g + 8], so a lane reads all it needs of a unit in one load.
+// Scales (16 bits) and zero points (8 bits) of a record are [g][group][row g,
+// row g + 8], so a lane reads all it needs of either in one load.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -32,13 +34,17 @@ namespace flashspmm {
 
 constexpr int kW4StripRows = 16;
 constexpr int kW4UnitCols = 128;
-constexpr int kW4UnitBytes = 1024;
+constexpr int kW4CodeBytes = 1024;  // of a record
+
+__host__ __device__ constexpr int32_t w4_record_bytes(int groups, bool zeros) {
+  return kW4CodeBytes + 32 * groups + (zeros ? 16 * groups : 0);
+}
 
 // A stack of 4-bit matrices as the kernels see it.
 struct W4Dev {
-  const uint4* codes;
-  const uint16_t* scales;
-  const uint8_t* zeros;  // nullptr: every zero point is 8
+  const uint8_t* data;
+  int32_t record;  // bytes
+  bool zeros;      // without them every zero point is 8
   int32_t M, K;
   int32_t strips;  // of one matrix that hold rows (the layout pads them to whole blocks)
   int32_t blocks;  // of one matrix
@@ -49,6 +55,7 @@ struct W4Dev {
   __device__ __forceinline__ int64_t unit(int64_t matrix, int32_t strip, int32_t u) const {
     return ((matrix * blocks + (strip >> 3)) * units + u) * 8 + (strip & 7);
   }
+  __device__ __forceinline__ const uint8_t* at(int64_t unit) const { return data + unit * record; }
 };
 
 __host__ __device__ inline int32_t w4_strips(int32_t M) {
@@ -63,9 +70,9 @@ __host__ __device__ inline int32_t w4_units(int32_t K) {
 
 inline W4Dev w4_dev(const flashspmm_w4* A) {
   W4Dev d;
-  d.codes = static_cast<const uint4*>(A->codes);
-  d.scales = static_cast<const uint16_t*>(A->scales);
-  d.zeros = A->zeros;
+  d.data = static_cast<const uint8_t*>(A->data);
+  d.record = w4_record_bytes(kW4UnitCols / A->group, A->zeros != 0);
+  d.zeros = A->zeros != 0;
   d.M = A->M;
   d.K = A->K;
   d.strips = w4_strips(A->M);
@@ -188,10 +195,29 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c = a (16 x 16) * b (16 x 8)
+template <typename T>
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816_zero<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+template <>
+__device__ __forceinline__ void mma16816_zero<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // ---------------------------------------------------------------- loads
 
 // Codes are read once: keep them out of L1, where the activations live.
-__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -222,26 +248,24 @@ struct W4Groups {
   uint32_t s[NG];            // {row g, row g + 8} in 16 bits each
   uint32_t z[(NG + 1) / 2];  // {row g, row g + 8} in 8 bits each, two groups to a word
 
-  __device__ __forceinline__ void load(const W4Dev& A, int64_t unit, int g) {
-    const int64_t at = (unit * 8 + g) * (NG * 2);
-    load(A.scales + at, A.zeros ? A.zeros + at : nullptr);
-  }
-  __device__ __forceinline__ void load(const uint16_t* sp, const uint8_t* zp) {
+  __device__ __forceinline__ void load(const uint8_t* record, int g, bool zeros) {
+    const uint8_t* sp = record + kW4CodeBytes + g * (4 * NG);
+    const uint8_t* zp = record + kW4CodeBytes + 32 * NG + g * (2 * NG);
     if (NG == 1) {
       s[0] = *reinterpret_cast<const uint32_t*>(sp);
-      z[0] = zp ? *reinterpret_cast<const uint16_t*>(zp) : 0x0808u;
+      z[0] = zeros ? *reinterpret_cast<const uint16_t*>(zp) : 0x0808u;
     } else if (NG == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(sp);
       s[0] = v.x;
       s[NG - 1] = v.y;
-      z[0] = zp ? *reinterpret_cast<const uint32_t*>(zp) : 0x08080808u;
+      z[0] = zeros ? *reinterpret_cast<const uint32_t*>(zp) : 0x08080808u;
     } else {
       const uint4 v = *reinterpret_cast<const uint4*>(sp);
       s[0] = v.x;
       s[1 % NG] = v.y;
       s[2 % NG] = v.z;
       s[NG - 1] = v.w;
-      const uint2 q = zp ? *reinterpret_cast<const uint2*>(zp) : make_uint2(0x08080808u, 0x08080808u);
+      const uint2 q = zeros ? *reinterpret_cast<const uint2*>(zp) : make_uint2(0x08080808u, 0x08080808u);
       z[0] = q.x;
       z[(NG - 1) / 2] = q.y;
     }
@@ -333,7 +357,7 @@ constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
 
 struct MoeCall {
-  flashspmm_w4 gate, up, down;  // up.codes null: no gate product
+  flashspmm_w4 gate, up, down;  // up.data null: no gate product
   const void* X;
   int64_t ldx;
   const void* router;  // null: ids and weights are inputs

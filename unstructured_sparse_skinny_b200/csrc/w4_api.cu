@@ -25,12 +25,12 @@ flashspmm_status check_shape(int32_t M, int32_t K, int32_t count, int32_t group)
 }
 
 flashspmm_status check_w4(const flashspmm_w4* A) {
-  if (!A || A->reserved != 0) return FLASHSPMM_ERR_INVALID_ARG;
+  if (!A || A->zeros < 0 || A->zeros > 1) return FLASHSPMM_ERR_INVALID_ARG;
   const flashspmm_status st = check_shape(A->M, A->K, A->count, A->group);
   if (st != FLASHSPMM_OK) return st;
   if (A->dtype != FLASHSPMM_F16 && A->dtype != FLASHSPMM_BF16) return FLASHSPMM_ERR_UNSUPPORTED;
-  if (A->M > 0 && A->K > 0 && (!A->codes || !A->scales)) return FLASHSPMM_ERR_INVALID_ARG;
-  if (!aligned16(A->codes) || !aligned16(A->scales) || !aligned16(A->zeros)) return FLASHSPMM_ERR_ALIGNMENT;
+  if (A->M > 0 && A->K > 0 && !A->data) return FLASHSPMM_ERR_INVALID_ARG;
+  if (!aligned16(A->data)) return FLASHSPMM_ERR_ALIGNMENT;
   return FLASHSPMM_OK;
 }
 
@@ -41,22 +41,16 @@ bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 extern "C" {
 
-int flashspmm_w4_sizes(int32_t M, int32_t K, int32_t count, int32_t group, int64_t* codes_bytes, int64_t* scales,
-                       int64_t* zeros) {
-  if (check_shape(M, K, count, group) != FLASHSPMM_OK) return -1;
-  const int64_t units = static_cast<int64_t>(count) * w4_blocks(M) * 8 * w4_units(K);
-  const int64_t groups = units * kW4StripRows * (kW4UnitCols / group);
-  if (codes_bytes) *codes_bytes = units * kW4UnitBytes;
-  if (scales) *scales = groups;
-  if (zeros) *zeros = groups;
-  return 0;
+int64_t flashspmm_w4_bytes(int32_t M, int32_t K, int32_t count, int32_t group, int32_t zeros) {
+  if (check_shape(M, K, count, group) != FLASHSPMM_OK || zeros < 0 || zeros > 1) return -1;
+  return static_cast<int64_t>(count) * w4_blocks(M) * 8 * w4_units(K) * w4_record_bytes(kW4UnitCols / group, zeros != 0);
 }
 
 flashspmm_status flashspmm_w4_encode(const void* W, int64_t ldw, int32_t symmetric, const flashspmm_w4* A,
                                      void* stream) {
   const flashspmm_status st = check_w4(A);
   if (st != FLASHSPMM_OK) return st;
-  if (ldw < A->K || (symmetric != 0) != (A->zeros == nullptr)) return FLASHSPMM_ERR_INVALID_ARG;
+  if (ldw < A->K || (symmetric != 0) != (A->zeros == 0)) return FLASHSPMM_ERR_INVALID_ARG;
   if (A->M == 0 || A->K == 0) return FLASHSPMM_OK;
   if (!W) return FLASHSPMM_ERR_INVALID_ARG;
   if (!on2(W)) return FLASHSPMM_ERR_ALIGNMENT;
@@ -68,7 +62,7 @@ flashspmm_status flashspmm_w4_pack(const uint8_t* codes, const void* scales, con
                                    const flashspmm_w4* A, void* stream) {
   const flashspmm_status st = check_w4(A);
   if (st != FLASHSPMM_OK) return st;
-  if ((zeros == nullptr) != (A->zeros == nullptr)) return FLASHSPMM_ERR_INVALID_ARG;
+  if ((zeros == nullptr) != (A->zeros == 0)) return FLASHSPMM_ERR_INVALID_ARG;
   if (A->M == 0 || A->K == 0) return FLASHSPMM_OK;
   if (!codes || !scales) return FLASHSPMM_ERR_INVALID_ARG;
   if (!on2(scales)) return FLASHSPMM_ERR_ALIGNMENT;

@@ -41,6 +41,20 @@ __device__ __forceinline__ void pack_block(const uint32_t (&q)[2][8], uint32_t& 
   w1 = w[1];
 }
 
+// A lane's share of a record.
+__device__ __forceinline__ void put_codes(uint8_t* record, int lane, const uint32_t (&w)[8]) {
+  reinterpret_cast<uint4*>(record)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(record)[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+// Scales and zero points of rows g and g + 8 for one group.
+template <int NG>
+__device__ __forceinline__ void put_group(uint8_t* record, int g, int group, uint32_t scales, uint32_t points,
+                                          bool zeros) {
+  const int o = g * (2 * NG) + 2 * group;
+  *reinterpret_cast<uint32_t*>(record + kW4CodeBytes + 2 * o) = scales;
+  if (zeros) *reinterpret_cast<uint16_t*>(record + kW4CodeBytes + 32 * NG + o) = static_cast<uint16_t>(points);
+}
+
 __device__ __forceinline__ uint32_t code_of(uint32_t w0, uint32_t w1, int row, int col) {
   const uint32_t w = col < 4 ? w0 : w1;
   const int c = col & 3;
@@ -78,8 +92,7 @@ struct Place {
 // 1.5 * 2^23 - 1536 then rounds to the even integer.
 template <typename T, int NG, bool Sym, bool Vec>
 __global__ void __launch_bounds__(kWarps * 32) w4_encode_kernel(const uint16_t* __restrict__ W, int64_t ldw, W4Dev A,
-                                                                uint4* codes, uint16_t* scales, uint8_t* zeros,
-                                                                int64_t total) {
+                                                                uint8_t* data, int64_t total) {
   constexpr int kBlocks = 4 / NG;  // 32-column blocks of a group
   const int lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -93,6 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32) w4_encode_kernel(const uint16_t* 
       raw[0][b] = load_act8<Vec>(r0, at.col0 + 32 * b, A.K);
       raw[1][b] = load_act8<Vec>(r1, at.col0 + 32 * b, A.K);
     }
+    uint8_t* record = data + unit * A.record;
     uint32_t words[8];
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
@@ -152,19 +166,16 @@ __global__ void __launch_bounds__(kWarps * 32) w4_encode_kernel(const uint16_t* 
       for (int b = 0; b < kBlocks; ++b)
         pack_block(q[b], words[2 * (gi * kBlocks + b)], words[2 * (gi * kBlocks + b) + 1]);
       if ((lane & 3) == 0) {
-        const int64_t o = (unit * 8 + (lane >> 2)) * (2 * NG) + 2 * gi;
         union {
           T t[2];
           uint32_t u;
         } pair;
         pair.t[0] = from_float<T>(s[0]);
         pair.t[1] = from_float<T>(s[1]);
-        *reinterpret_cast<uint32_t*>(scales + o) = pair.u;
-        if (!Sym) *reinterpret_cast<uint16_t*>(zeros + o) = static_cast<uint16_t>(zp[0] | (zp[1] << 8));
+        put_group<NG>(record, lane >> 2, gi, pair.u, zp[0] | (zp[1] << 8), !Sym);
       }
     }
-    codes[unit * 64 + lane] = make_uint4(words[0], words[1], words[2], words[3]);
-    codes[unit * 64 + 32 + lane] = make_uint4(words[4], words[5], words[6], words[7]);
+    put_codes(record, lane, words);
   }
 }
 
@@ -174,8 +185,7 @@ template <int NG, bool Vec>
 __global__ void __launch_bounds__(kWarps * 32) w4_pack_kernel(const uint8_t* __restrict__ in,
                                                               const uint16_t* __restrict__ in_scales,
                                                               const uint8_t* __restrict__ in_zeros, W4Dev A,
-                                                              uint4* codes, uint16_t* scales, uint8_t* zeros,
-                                                              int64_t total) {
+                                                              uint8_t* data, int64_t total) {
   const int lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t groups = (static_cast<int64_t>(A.K) + A.group - 1) / A.group;
@@ -216,15 +226,12 @@ __global__ void __launch_bounds__(kWarps * 32) w4_pack_kernel(const uint8_t* __r
       }
       pack_block(q, words[2 * b], words[2 * b + 1]);
     }
-    codes[unit * 64 + lane] = make_uint4(words[0], words[1], words[2], words[3]);
-    codes[unit * 64 + 32 + lane] = make_uint4(words[4], words[5], words[6], words[7]);
+    uint8_t* record = data + unit * A.record;
+    put_codes(record, lane, words);
     if ((lane & 3) == 0) {
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        const int64_t o = (unit * 8 + (lane >> 2)) * (2 * NG) + 2 * gi;
-        *reinterpret_cast<uint32_t*>(scales + o) = sc[0][gi] | (sc[1][gi] << 16);
-        if (zeros) *reinterpret_cast<uint16_t*>(zeros + o) = static_cast<uint16_t>(zp[0][gi] | (zp[1][gi] << 8));
-      }
+      for (int gi = 0; gi < NG; ++gi)
+        put_group<NG>(record, lane >> 2, gi, sc[0][gi] | (sc[1][gi] << 16), zp[0][gi] | (zp[1][gi] << 8), A.zeros);
     }
   }
 }
@@ -255,8 +262,9 @@ __global__ void __launch_bounds__(kWarps * 32) w4_decode_kernel(W4Dev A, O* __re
   for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); unit < total; unit += step) {
     const Place at(A, unit, lane);
     W4Groups<T, NG> grp;
-    grp.load(A, unit, lane >> 2);
-    const uint4 c0 = ld_stream(A.codes + unit * 64 + lane), c1 = ld_stream(A.codes + unit * 64 + 32 + lane);
+    const uint8_t* record = A.at(unit);
+    grp.load(record, lane >> 2, A.zeros);
+    const uint4 c0 = ld_stream(record + lane * 16), c1 = ld_stream(record + 512 + lane * 16);
     const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -293,11 +301,9 @@ int grid_for(int64_t units) {
 template <typename T, int NG>
 void encode_as(const uint16_t* W, int64_t ldw, const W4Dev& A, const flashspmm_w4* out, bool sym, bool vec,
                int64_t total, cudaStream_t s) {
-  uint4* codes = static_cast<uint4*>(out->codes);
-  uint16_t* scales = static_cast<uint16_t*>(out->scales);
+  uint8_t* data = static_cast<uint8_t*>(out->data);
   const int grid = grid_for(total);
-#define FLASHSPMM_ENCODE(SYM, VEC) \
-  w4_encode_kernel<T, NG, SYM, VEC><<<grid, kWarps * 32, 0, s>>>(W, ldw, A, codes, scales, out->zeros, total)
+#define FLASHSPMM_ENCODE(SYM, VEC) w4_encode_kernel<T, NG, SYM, VEC><<<grid, kWarps * 32, 0, s>>>(W, ldw, A, data, total)
   if (sym)
     vec ? FLASHSPMM_ENCODE(true, true) : FLASHSPMM_ENCODE(true, false);
   else
@@ -358,12 +364,11 @@ cudaError_t launch_w4_pack(const uint8_t* in, const void* in_scales, const uint8
   const int64_t total = all_units(out);
   const bool vec = (reinterpret_cast<uintptr_t>(in) & 7u) == 0 && A.K % 8 == 0;
   const uint16_t* sc = static_cast<const uint16_t*>(in_scales);
-  uint4* codes = static_cast<uint4*>(out->codes);
-  uint16_t* scales = static_cast<uint16_t*>(out->scales);
+  uint8_t* data = static_cast<uint8_t*>(out->data);
   const int grid = grid_for(total);
-#define FLASHSPMM_PACK(NG)                                                                                            \
-  vec ? w4_pack_kernel<NG, true><<<grid, kWarps * 32, 0, s>>>(in, sc, in_zeros, A, codes, scales, out->zeros, total)  \
-      : w4_pack_kernel<NG, false><<<grid, kWarps * 32, 0, s>>>(in, sc, in_zeros, A, codes, scales, out->zeros, total)
+#define FLASHSPMM_PACK(NG)                                                                          \
+  vec ? w4_pack_kernel<NG, true><<<grid, kWarps * 32, 0, s>>>(in, sc, in_zeros, A, data, total)     \
+      : w4_pack_kernel<NG, false><<<grid, kWarps * 32, 0, s>>>(in, sc, in_zeros, A, data, total)
   if (A.group == 128)
     FLASHSPMM_PACK(1);
   else if (A.group == 64)

@@ -90,13 +90,6 @@ __global__ void __launch_bounds__(256) w4_stage_kernel(const uint16_t* __restric
 
 // ---------------------------------------------------------------- primitives
 
-__device__ __forceinline__ void bulk_load(void* smem, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // 16 TMEM lanes x 32 columns: register 2 i is row g, 2 i + 1 row g + 8 of column 4 i + t.
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -138,13 +131,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s, __nv_bfloat16) 
   return r;
 }
 
-// A block's unit in shared memory: codes, scales, zero points of its 8 strips.
-template <int NG>
-struct Shared {
-  static constexpr int kCodes = 8 * kW4UnitBytes, kScales = 8 * 16 * NG * 2, kZeros = 8 * 16 * NG;
-  static constexpr int kBytes = kCodes + kScales + kZeros;
-};
-
 // The P-th part (128 / P columns) of one strip of it as a lane holds it: codes, then 16-bit weights.
 template <typename T, int NG, int P>
 struct Part {
@@ -153,22 +139,21 @@ struct Part {
   uint32_t w[kWords];
   uint32_t s[kGroups], z[kGroups];                       // {row g, row g + 8}
 
-  __device__ __forceinline__ void load(const uint8_t* unit, int strip, int part, int lane, bool zeros) {
+  __device__ __forceinline__ void load(const uint8_t* record, int part, int lane, bool zeros) {
     if (P == 2) {
-      const uint4 v = *reinterpret_cast<const uint4*>(unit + strip * kW4UnitBytes + part * 512 + lane * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(record + part * 512 + lane * 16);
       w[0] = v.x;
       w[1] = v.y;
       w[2 % kWords] = v.z;
       w[3 % kWords] = v.w;
     } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(unit + strip * kW4UnitBytes + (part >> 1) * 512 + lane * 16 +
-                                                      (part & 1) * 8);
+      const uint2 v = *reinterpret_cast<const uint2*>(record + (part >> 1) * 512 + lane * 16 + (part & 1) * 8);
       w[0] = v.x;
       w[1] = v.y;
     }
-    const int at = (strip * 8 + (lane >> 2)) * (2 * NG) + 2 * (part * NG / P);
-    const uint8_t* scales = unit + Shared<NG>::kCodes + at * 2;
-    const uint8_t* points = unit + Shared<NG>::kCodes + Shared<NG>::kScales + at;
+    const int at = (lane >> 2) * (2 * NG) + 2 * (part * NG / P);
+    const uint8_t* scales = record + kW4CodeBytes + at * 2;
+    const uint8_t* points = record + kW4CodeBytes + 32 * NG + at;
     if (kGroups == 1) {
       s[0] = *reinterpret_cast<const uint32_t*>(scales);
       z[0] = zeros ? *reinterpret_cast<const uint16_t*>(points) : 0x0808u;
@@ -377,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   const int32_t units = p.A.units;
   const Runs runs(p.steps, gridDim.x);
   const int32_t q0 = runs.begin(blockIdx.x), q1 = runs.begin(blockIdx.x + 1);
-  const uint32_t stage_bytes = static_cast<uint32_t>(p.n_pad) * 256;
+  const uint32_t stage_bytes = static_cast<uint32_t>(p.n_pad) * 256, unit_bytes = 8 * p.A.record;
   const Accumulators acc(p.n_pad);
   uint8_t* tiles = smem + ((1024 - (smem_u32(smem) & 1023)) & 1023);
   uint8_t* codes = tiles + p.slots * stage_bytes;
@@ -415,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     const int quad = warp & 3, part = (warp >> 2) % P, group = (warp >> 2) / P;
     const uint32_t dst =
         tmem + kAccCols + part * (kUnitTmemCols / P) + (static_cast<uint32_t>(quad * 32) << 16);
-    const bool zeros = p.A.zeros != nullptr;
+    const bool zeros = p.A.zeros;
+    const uint8_t* mine = codes + quad * 2 * p.A.record;
     uint32_t phase = 1, ring_phase = 0;
     int ring = group, slot = group;
     for (int32_t q = q0 + group; q < q1; q += kGroups) {
@@ -425,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         Part<T, NG, P> strip;
-        strip.load(codes + ring * Shared<NG>::kBytes, quad * 2 + j, part, lane, zeros);
+        strip.load(mine + ring * unit_bytes + j * p.A.record, part, lane, zeros);
         strip.weights(r[j]);
       }
       if (!mbar_wait(&used[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
@@ -538,16 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     const int slots = of_codes ? p.ring : p.slots;
     uint64_t* filled = of_codes ? codes_full : full;
     uint64_t* freed = of_codes ? codes_used : used;
-    const uint32_t zero_bytes = p.A.zeros ? Shared<NG>::kZeros : 0;
-    const uint32_t bytes = of_codes ? Shared<NG>::kCodes + Shared<NG>::kScales + zero_bytes : stage_bytes;
+    const uint32_t bytes = of_codes ? unit_bytes : stage_bytes;
     // a block's units are consecutive: step q is the matrix's q-th
-    const int64_t first = q0;
-    const uint8_t* from =
-        of_codes ? reinterpret_cast<const uint8_t*>(p.A.codes) + first * Shared<NG>::kCodes : p.image;
-    const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.A.scales) + first * Shared<NG>::kScales;
-    const uint8_t* points = p.A.zeros + first * Shared<NG>::kZeros;
     int32_t u = q0 % units;
-    if (!of_codes) from += static_cast<int64_t>(u) * stage_bytes;
+    const uint8_t* from = of_codes ? p.A.data + static_cast<int64_t>(q0) * unit_bytes
+                                   : p.image + static_cast<int64_t>(u) * stage_bytes;
+    uint8_t* to = of_codes ? codes : tiles;
     int32_t left = q1 - q0;
     int slot = 0, issued = 0;
     uint32_t phase = 1;
@@ -555,27 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
       if (!mbar_wait(&freed[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&filled[slot], bytes);
-        if (of_codes) {
-          uint8_t* to = codes + slot * Shared<NG>::kBytes;
-          bulk_load(to, from, Shared<NG>::kCodes, &filled[slot]);
-          bulk_load(to + Shared<NG>::kCodes, scales, Shared<NG>::kScales, &filled[slot]);
-          if (zero_bytes)
-            bulk_load(to + Shared<NG>::kCodes + Shared<NG>::kScales, points, zero_bytes, &filled[slot]);
-        } else {
-          bulk_load(tiles + slot * stage_bytes, from, stage_bytes, &filled[slot]);
-        }
+        bulk_load(to + slot * bytes, from, bytes, &filled[slot]);
       }
       __syncwarp();
-      if (of_codes) {
-        from += Shared<NG>::kCodes;
-        scales += Shared<NG>::kScales;
-        points += Shared<NG>::kZeros;
-      } else {
-        from += stage_bytes;
-        if (++u == units) {
-          u = 0;
-          from = p.image;
-        }
+      from += bytes;
+      if (++u == units) {
+        u = 0;
+        if (!of_codes) from = p.image;
       }
       if (issued < slots) ++issued;
       if (++slot == slots) {
@@ -648,7 +616,7 @@ cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
   // P = 2: four units between codes and product, two to a group of warps, so one is turned into weights while
   // the products of the other run.  P = 4, for tiles of which only three fit: all warps on each unit.
   p.slots = P == 2 ? 4 : 3;
-  p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * p.n_pad * 256) / Shared<NG>::kBytes)) / 4 *
+  p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * p.n_pad * 256) / (8 * p.A.record))) / 4 *
            4 * (P == 2) + 3 * (P == 4);
   auto kernel = w4_gemm_kernel<T, NG, P>;
   static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
@@ -663,7 +631,7 @@ cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.slots) * p.n_pad * 256 + p.ring * Shared<NG>::kBytes + 1024;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.slots) * p.n_pad * 256 + p.ring * 8 * p.A.record + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -25,17 +25,18 @@ struct MatmulParams {
 // 29 and 54 us for one and eight tokens of 12288^2.)
 template <typename T, int NG>
 __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const MatmulParams p) {
-  constexpr int kAhead = 2, kBlocks = 4 / NG;
+  constexpr int kAhead = 2;
   __shared__ float red[kMatmulWarps][8][20];  // 16 rows, and the fragments' stores meet all banks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const StripAt at(p.A, p.A.unit(0, blockIdx.x, 0), lane);
+  const uint8_t* strip = p.A.at(p.A.unit(0, blockIdx.x, 0));
+  const int32_t pitch = 8 * p.A.record;  // from a strip's unit to its next
   const int32_t units = p.A.units;
   const uint16_t* row = g < p.N ? p.B + g * p.ldb + 8 * t : nullptr;
   StripUnit<T, NG> buf[kAhead];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
-    if (warp + d * kMatmulWarps < units) buf[d].load(at, warp + d * kMatmulWarps);
-  float acc[4] = {};
+    if (warp + d * kMatmulWarps < units) buf[d].load(strip + static_cast<int64_t>(warp + d * kMatmulWarps) * pitch, lane, p.A.zeros);
+  float acc[1][4] = {};
   for (int32_t base = warp; base < units; base += kAhead * kMatmulWarps) {
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
@@ -47,33 +48,13 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
         x[b] = make_uint4(0, 0, 0, 0);
         if (row && u * 128 + 32 * b + 8 * t < p.A.K) x[b] = __ldg(reinterpret_cast<const uint4*>(row + u * 128 + 32 * b));
       }
-#pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        const W4Zero<T> z = buf[d].g.zero(gi);
-        float sum[4];
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int blk = gi * kBlocks + b;
-          uint32_t a[2][4];
-          w4_fragment(buf[d].word(2 * blk), z, a[0]);
-          w4_fragment(buf[d].word(2 * blk + 1), z, a[1]);
-          if (b == 0)
-            mma16816_zero<T>(sum, a[0], x[blk].x, x[blk].y);
-          else
-            mma16816<T>(sum, a[0], x[blk].x, x[blk].y);
-          mma16816<T>(sum, a[1], x[blk].z, x[blk].w);
-        }
-        const float s0 = buf[d].g.scale(gi, 0), s1 = buf[d].g.scale(gi, 1);
-        acc[0] = fmaf(s0, sum[0], acc[0]);
-        acc[1] = fmaf(s0, sum[1], acc[1]);
-        acc[2] = fmaf(s1, sum[2], acc[2]);
-        acc[3] = fmaf(s1, sum[3], acc[3]);
-      }
-      if (u + kAhead * kMatmulWarps < units) buf[d].load(at, u + kAhead * kMatmulWarps);
+      strip_unit<T, NG, 1>(buf[d], 1, [&](int, int b) { return x[b]; }, acc);
+      const int32_t next = u + kAhead * kMatmulWarps;
+      if (next < units) buf[d].load(strip + static_cast<int64_t>(next) * pitch, lane, p.A.zeros);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[i];
+  for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[0][i];
   __syncthreads();
   if (threadIdx.x < 128) {
     const int n = threadIdx.x >> 4, r = threadIdx.x & 15;

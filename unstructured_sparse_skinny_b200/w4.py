@@ -29,52 +29,43 @@ _ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 
 class _W4View(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("count", ctypes.c_int32), ("group", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p),
-                ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+                ("dtype", ctypes.c_int32), ("zeros", ctypes.c_int32), ("data", ctypes.c_void_p)]
 
 
 @dataclass(frozen=True, eq=False)
 class W4:
     """A 4-bit matrix [M, K], or a stack [count, M, K], in device memory."""
-    codes: torch.Tensor          # uint8 [count, blocks, units, 8, 1024]: blocks of 128 rows, units of 128 columns
-    scales: torch.Tensor         # float16 or bfloat16 [count, blocks, units, 8, 8, 128 // group, 2]
-    zeros: torch.Tensor | None   # uint8, the scales' shape; None: every zero point is 8
+    data: torch.Tensor   # uint8 [count, blocks, units, 8, record]: blocks of 128 rows, units of 128 columns
+    dtype: torch.dtype   # of the scales, and of the activations they meet: float16 or bfloat16
     M: int
     K: int
     group: int
-    stacked: bool = False        # made from a 3-D tensor
+    symmetric: bool      # without zero points: every one is 8
+    stacked: bool = False  # made from a 3-D tensor
     _ref: object = field(default=None, init=False, repr=False)
 
     def __post_init__(self):
-        z = self.zeros
-        v = _W4View(self.M, self.K, self.codes.shape[0], self.group, _DTYPES[self.scales.dtype], 0,
-                    self.codes.data_ptr() or None, self.scales.data_ptr() or None,
-                    None if z is None else z.data_ptr() or None)
+        v = _W4View(self.M, self.K, self.data.shape[0], self.group, _DTYPES[self.dtype], int(not self.symmetric),
+                    self.data.data_ptr() or None)
         object.__setattr__(self, "_ref", ctypes.byref(v))  # byref keeps the structure alive
 
     @property
     def count(self) -> int:
-        return int(self.codes.shape[0])
-
-    @property
-    def dtype(self) -> torch.dtype:
-        return self.scales.dtype
+        return int(self.data.shape[0])
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self.data.device
 
     @property
     def nbytes(self) -> int:
-        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.zeros) if t is not None)
+        return int(self.data.numel())
 
     def matrix(self, index: int) -> "W4":
         """One matrix of a stack as a view; nothing is copied."""
         if not 0 <= index < self.count:
             raise IndexError(f"matrix {index} of a stack of {self.count}")
-        part = slice(index, index + 1)
-        return W4(self.codes[part], self.scales[part], None if self.zeros is None else self.zeros[part], self.M,
-                  self.K, self.group)
+        return W4(self.data[index:index + 1], self.dtype, self.M, self.K, self.group, self.symmetric)
 
 
 class _On:
@@ -138,17 +129,16 @@ def _output(t, shape: tuple, dtypes, device: torch.device, name: str) -> int:
 
 
 def _empty(shape, dtype: torch.dtype, group: int, symmetric: bool, device: torch.device) -> W4:
-    """Unwritten buffers for a weight of shape [M, K] or [count, M, K]."""
-    lib = binding.load_library()
+    """Unwritten data for a weight of shape [M, K] or [count, M, K]."""
     count, (M, K) = (shape[0] if len(shape) == 3 else 1), shape[-2:]
-    if lib.flashspmm_w4_sizes(M, K, count, group, None, None, None) != 0:
+    nbytes = binding.load_library().flashspmm_w4_bytes(M, K, count, group, int(not symmetric))
+    if nbytes < 0:
         raise ValueError(f"4-bit weights need group 32, 64 or 128 and at least one matrix, got group {group}, "
                          f"shape {tuple(shape)}")
     blocks, units = -(-M // 128), -(-K // 128)
-    per = (count, blocks, units, 8, 8, 128 // group, 2)
-    return W4(torch.empty((count, blocks, units, 8, 1024), dtype=torch.uint8, device=device),
-              torch.empty(per, dtype=dtype, device=device),
-              None if symmetric else torch.empty(per, dtype=torch.uint8, device=device), M, K, group, len(shape) == 3)
+    record = nbytes // max(1, count * blocks * units * 8)
+    return W4(torch.empty((count, blocks, units, 8, record), dtype=torch.uint8, device=device), dtype, M, K, group,
+              symmetric, len(shape) == 3)
 
 
 def w4_encode(W: torch.Tensor, group: int = 128, symmetric: bool = True, stream=None) -> W4:
@@ -220,7 +210,7 @@ def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None
     (rows may be apart); returns C as ``[N, M]`` in that type, or writes the
     given C, which may be float32 (the unrounded sums)."""
     lib = binding._lib or binding.load_library()
-    device, dtype = A.codes.device, A.scales.dtype
+    device, dtype = A.data.device, A.dtype
     if B.dtype is not dtype or B.dim() != 2 or B.device != device:
         raise TypeError(f"B must be a 2-D {dtype} tensor on {device}")
     if _elsewhere(device, stream):
@@ -247,7 +237,7 @@ def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None
 
 def _moe(X, router, gate, up, down, top_k, renormalize, activation, ids, weights, out):
     lib = binding._lib or binding.load_library()
-    device, dtype = gate.codes.device, gate.scales.dtype
+    device, dtype = gate.data.device, gate.dtype
     X, ldx = _rows(X)
     T = X.shape[0]
     if out is None:
@@ -267,7 +257,7 @@ def _moe(X, router, gate, up, down, top_k, renormalize, activation, ids, weights
 
 
 def _check_experts(X, gate: W4, up, down: W4, activation: str) -> None:
-    device, dtype = gate.codes.device, gate.scales.dtype
+    device, dtype = gate.data.device, gate.dtype
     if X.dtype is not dtype or X.dim() != 2 or X.device != device:
         raise TypeError(f"X must be a 2-D {dtype} tensor on {device}")
     if X.shape[1] != gate.K:
@@ -275,7 +265,7 @@ def _check_experts(X, gate: W4, up, down: W4, activation: str) -> None:
     if activation not in _ACTIVATIONS:
         raise ValueError("activation must be one of " + ", ".join(_ACTIVATIONS))
     for w in (up, down):
-        if w is not None and w.codes.device != device:
+        if w is not None and w.data.device != device:
             raise ValueError("the experts' weights must be on one device")
 
 
@@ -291,9 +281,9 @@ def moe_w4(X: torch.Tensor, router: torch.Tensor, gate: W4, up: W4 | None, down:
     "silu", "gelu" (with erf) or "relu".  ``ids`` is int32 and ``weights``
     float32, both ``[T, top_k]``, the largest first."""
     _check_experts(X, gate, up, down, activation)
-    device = gate.codes.device
+    device = gate.data.device
     if (router.dtype is not X.dtype and router.dtype is not torch.float32) or router.device != device or \
-            router.shape != (gate.codes.shape[0], gate.K):
+            router.shape != (gate.data.shape[0], gate.K):
         raise TypeError(f"router must be a [{gate.count}, {gate.K}] tensor of X's type or float32 on {device}")
     if _elsewhere(device, stream):
         with _On(device, stream):
@@ -313,7 +303,7 @@ def moe_w4_experts(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, ga
     or an expert of another rank) contributes nothing; a token whose ids are
     all outside gets zeros."""
     _check_experts(X, gate, up, down, activation)
-    device = gate.codes.device
+    device = gate.data.device
     _cuda(ids, "ids", (torch.int32, ))
     _cuda(weights, "weights", (torch.float32, ))
     if ids.dim() != 2 or ids.shape[0] != X.shape[0] or weights.shape != ids.shape or ids.device != device or \

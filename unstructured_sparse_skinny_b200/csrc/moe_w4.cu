@@ -340,7 +340,7 @@ struct ExpertParams {
   int64_t ldx;
   int32_t H;             // columns of X that may be read
   int32_t activation;
-  int32_t slots;         // strips a CTA takes
+  int32_t pairs;         // of strips a CTA takes
   uint32_t shared;
   Workspace ws;
 };
@@ -355,29 +355,33 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
   griddep_launch_dependents();
   if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
   const Slot slot = p.ws.slots[blockIdx.y];
-  // with a gate product neighbouring warps have the same strip of gate and of up
-  const int w = (threadIdx.x >> 5) % p.slots;
-  const int32_t strip0 = blockIdx.x * (Gated ? p.slots / 2 : p.slots);
-  const W4Dev& A = Gated && (w & 1) ? p.up : p.gate;
-  const uint8_t* strip = A.at(A.unit(slot.expert, min(strip0 + (Gated ? w >> 1 : w), A.strips - 1), 0));
+  const W4Dev& A = p.gate;
+  const int32_t pair0 = blockIdx.x * p.pairs, pair = pair0 + (threadIdx.x >> 5) % p.pairs, last = A.strips - 1;
+  // a warp's strips: the same of gate and up, or without a gate product neighbours
+  const int64_t unit0 = A.unit(slot.expert, min(Gated ? pair : 2 * pair, last), 0);
+  const int64_t unit1 = Gated ? unit0 : A.unit(slot.expert, min(2 * pair + 1, last), 0);
+  const StripAt at[2] = {StripAt(A, unit0), StripAt(Gated ? p.up : A, unit1)};
   if (threadIdx.x < slot.count) token[threadIdx.x] = p.ws.pair_token[slot.first + threadIdx.x];
   for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
     const int32_t rows = min(slot.count - n0, NT * 8);
-    float acc[NT][4] = {};
+    float acc[2][NT][4] = {};
     strip_product<T, NG, NT>(
-        strip, 8 * A.record, A.zeros, A.units, p.H, rows, p.slots, smem, p.shared,
-        [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
-    strip_reduce<NT, Gated>(acc, p.slots, rows, smem, [&](int s, int32_t n, int32_t row, float g, float u) {
-      const int32_t f = (strip0 + s) * 16 + row;
-      if (f >= p.ws.ldh) return;
-      const float v = activate(p.activation, g) * (Gated ? u : 1.0f);
+        at, A.units, p.H, rows, p.pairs, smem, p.shared, [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
+    const auto store = [&](int32_t n, int32_t f, float v) {
       // columns behind F pad h to 16 bytes: finite whatever x holds
-      reinterpret_cast<T*>(p.ws.h)[(slot.first + n0 + n) * p.ws.ldh + f] = from_float<T>(f < p.gate.M ? v : 0.0f);
+      if (f < p.ws.ldh)
+        reinterpret_cast<T*>(p.ws.h)[(slot.first + n0 + n) * p.ws.ldh + f] = from_float<T>(f < A.M ? v : 0.0f);
+    };
+    strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
+      const int32_t f = (pair0 + i) * (Gated ? 16 : 32) + row;
+      a = activate(p.activation, a);
+      store(n, f, Gated ? a * b : a);
+      if (!Gated) store(n, f + 16, activate(p.activation, b));
     });
   }
 }
 
-// y[pair] = weight * down h for some strips of a running expert.
+// y[pair] = weight * down h for some pairs of strips of a running expert.
 template <typename T, int NG, int NT>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -386,18 +390,21 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
   if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
   const Slot slot = p.ws.slots[blockIdx.y];
   const W4Dev& A = p.down;
-  const int32_t strip0 = blockIdx.x * p.slots;
-  const int w = (threadIdx.x >> 5) % p.slots;
-  const uint8_t* strip = A.at(A.unit(slot.expert, min(strip0 + w, A.strips - 1), 0));
+  const int32_t pair0 = blockIdx.x * p.pairs, pair = pair0 + (threadIdx.x >> 5) % p.pairs, last = A.strips - 1;
+  const StripAt at[2] = {StripAt(A, A.unit(slot.expert, min(2 * pair, last), 0)),
+                         StripAt(A, A.unit(slot.expert, min(2 * pair + 1, last), 0))};
   for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
     const int32_t rows = min(slot.count - n0, NT * 8), first = slot.first + n0;
-    float acc[NT][4] = {};
+    float acc[2][NT][4] = {};
     strip_product<T, NG, NT>(
-        strip, 8 * A.record, A.zeros, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.slots, smem, p.shared,
+        at, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, p.shared,
         [&](int32_t n) { return p.ws.h + (first + n) * p.ws.ldh; }, acc);
-    strip_reduce<NT, false>(acc, p.slots, rows, smem, [&](int s, int32_t n, int32_t row, float sum, float) {
-      const int32_t m = (strip0 + s) * 16 + row;
-      if (m < A.M) p.ws.y[static_cast<int64_t>(first + n) * A.M + m] = p.ws.pair_weight[first + n] * sum;
+    strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
+      const int32_t m = (pair0 + i) * 32 + row;
+      const float w = p.ws.pair_weight[first + n];
+      float* y = p.ws.y + static_cast<int64_t>(first + n) * A.M;
+      if (m < A.M) y[m] = w * a;
+      if (m + 16 < A.M) y[m + 16] = w * b;
     });
   }
 }
@@ -460,17 +467,20 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
   }
   const int64_t most = min64(c.gate.count, static_cast<int64_t>(c.tokens) * c.top_k);
   const int32_t rows = c.tokens < NT * 8 ? c.tokens : NT * 8;
-  int32_t strips = p.gate.strips * (gated ? 2 : 1);
-  p.slots = strips_per_cta(most, strips, 2);
+  // experts that run and their tokens, as even routing has them
+  const double E = c.gate.count, pairs = static_cast<double>(c.tokens) * c.top_k;
+  const double share = c.top_k < E ? c.top_k / E : 1.0, running = E * (1.0 - std::pow(1.0 - share, c.tokens));
+  int32_t all = gated ? p.gate.strips : (p.gate.strips + 1) / 2;
+  p.pairs = pairs_per_cta(running, all, p.gate.units, pairs / running);
   p.shared = strip_shared(rows, p.gate.units, NT);
-  e = launch_after(gate_up, dim3((strips + p.slots - 1) / p.slots, static_cast<unsigned>(most)), kStripThreads,
-                   p.shared, 1, s, p);
-  if (e != cudaSuccess) return e;
-  strips = p.down.strips;
-  p.slots = strips_per_cta(most, strips, 2);
-  p.shared = strip_shared(rows, p.down.units, NT);
-  e = launch_after(down, dim3((strips + p.slots - 1) / p.slots, static_cast<unsigned>(most)), kStripThreads, p.shared,
+  e = launch_after(gate_up, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
                    1, s, p);
+  if (e != cudaSuccess) return e;
+  all = (p.down.strips + 1) / 2;
+  p.pairs = pairs_per_cta(running, all, p.down.units, pairs / running);
+  p.shared = strip_shared(rows, p.down.units, NT);
+  e = launch_after(down, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared, 1,
+                   s, p);
   if (e != cudaSuccess) return e;
   return launch_after(moe_join_kernel<T>, dim3((p.down.M + 255) / 256, c.tokens), 256, 0, 1, s,
                       static_cast<const float*>(p.ws.y), static_cast<const int32_t*>(p.ws.place), c.top_k, p.down.M,

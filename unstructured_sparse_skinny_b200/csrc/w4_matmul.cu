@@ -32,11 +32,11 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
   const int32_t pitch = 8 * p.A.record;  // from a strip's unit to its next
   const int32_t units = p.A.units;
   const uint16_t* row = g < p.N ? p.B + g * p.ldb + 8 * t : nullptr;
-  StripUnit<T, NG> buf[kAhead];
+  StripUnit<T, NG> buf[kAhead][1];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
-    if (warp + d * kMatmulWarps < units) buf[d].load(strip + static_cast<int64_t>(warp + d * kMatmulWarps) * pitch, lane, p.A.zeros);
-  float acc[1][4] = {};
+    if (warp + d * kMatmulWarps < units) buf[d][0].load(strip + static_cast<int64_t>(warp + d * kMatmulWarps) * pitch, lane, p.A.zeros);
+  float acc[1][1][4] = {};
   for (int32_t base = warp; base < units; base += kAhead * kMatmulWarps) {
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
@@ -48,13 +48,13 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
         x[b] = make_uint4(0, 0, 0, 0);
         if (row && u * 128 + 32 * b + 8 * t < p.A.K) x[b] = __ldg(reinterpret_cast<const uint4*>(row + u * 128 + 32 * b));
       }
-      strip_unit<T, NG, 1>(buf[d], 1, [&](int, int b) { return x[b]; }, acc);
+      strip_unit<T, NG, 1, 1, 1>(buf[d], 1, [&](int, int b) { return x[b]; }, acc);
       const int32_t next = u + kAhead * kMatmulWarps;
-      if (next < units) buf[d].load(strip + static_cast<int64_t>(next) * pitch, lane, p.A.zeros);
+      if (next < units) buf[d][0].load(strip + static_cast<int64_t>(next) * pitch, lane, p.A.zeros);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[0][i];
+  for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[0][0][i];
   __syncthreads();
   if (threadIdx.x < 128) {
     const int n = threadIdx.x >> 4, r = threadIdx.x & 15;

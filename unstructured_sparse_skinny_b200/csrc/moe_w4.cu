@@ -1,16 +1,18 @@
 // A mixture-of-experts layer for a few tokens with 4-bit experts.
 //
-//   logits = router x            (64-bit sums: their order decides which experts run)
+//   logits = router x            (sums of 46 bits: their order decides which experts run)
 //   ids, p = top_k(logits)       (ties to the lower index), p = softmax over the chosen or over all
 //   h_e    = act(gate_e x) * (up_e x), or act(gate_e x)
 //   out    = sum over the token's experts of p * (down_e h_e)
 //
-// Five kernels, each started while the one before it ends: logits; routing,
-// which turns the choice into one list of tokens per running expert; gate and
-// up with the activation; down, weighted; and the sum over a token's experts.
-// Every expert's codes are read once however many of its tokens there are, and
-// every sum has a fixed order: no atomics on values.
+// Three to five kernels, each started while the one before it ends: logits;
+// routing, which turns the choice into one list of tokens per running expert
+// (and makes a small layer's logits too); gate and up with the activation; down,
+// weighted; and the sum over a token's experts, which up to eight tokens is part
+// of down.  An expert's codes are read once for every 8, 16 or 32 of its tokens,
+// and every sum has a fixed order: no atomics on values.
 #include <atomic>
+#include <type_traits>
 
 #include "w4_strips.cuh"
 
@@ -21,9 +23,11 @@ constexpr int kRouteWarps = 16;
 constexpr int kRouteThreads = kRouteWarps * 32;
 constexpr int kRouteCtas = 8;  // one cluster
 
-// An expert that runs: its tokens are pairs [first, first + count).
+// An expert that runs: its tokens are pairs [first, first + count), and their
+// bits among the first 32 tokens.
 struct __align__(16) Slot {
-  int32_t expert, first, count, pad;
+  int32_t expert, first, count;
+  uint32_t tokens;
 };
 
 struct Workspace {
@@ -102,11 +106,32 @@ struct RouterRow<float> {
   }
 };
 
+// A sum of some 46 bits in two fp32 words: the rounding of every addition is
+// computed (Knuth's two-sum) and added up beside.  64-bit arithmetic would do,
+// but the conversions to it run at some 5 a cycle and SM: 17 us for one token
+// and 128 experts of 2048 columns on a cluster, where this takes 3.
+struct Sum2 {
+  float s = 0.0f, c = 0.0f;
+  __device__ __forceinline__ void add(float p, float below) {
+    const float t = s + p, z = t - s;
+    c += ((s - (t - z)) + (p - z)) + below;
+    s = t;
+  }
+  // of an infinite sum the rounding is not a number, and not wanted
+  __device__ __forceinline__ double value() const {
+    return static_cast<double>(s) + static_cast<double>(c == c ? c : 0.0f);
+  }
+};
+// w * x: a product of two 16-bit values is exact in fp32, of an fp32 router's its rounding is kept.
+template <typename RT>
+__device__ __forceinline__ void add_product(Sum2& sum, float w, float x) {
+  const float p = w * x;
+  sum.add(p, std::is_same<RT, float>::value ? fmaf(w, x, -p) : 0.0f);
+}
+
 // A CTA has EB experts and TB tokens; its threads share the columns, eight
-// neighbours each.  A conversion to 64 bits costs four fused multiply-adds of
-// the same width, so a thread converts once for EB or TB products.  Equal
-// router rows give equal logits bit for bit: the order of a sum depends on H
-// and the tile's shape alone.
+// neighbours each.  Equal router rows give equal logits bit for bit: the order
+// of a sum depends on H and the tile's shape alone.
 template <typename T, typename RT, bool Vec, int EB, int TB>
 __global__ void __launch_bounds__(256) moe_logits_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                          const void* __restrict__ router, int32_t H, int32_t tokens,
@@ -115,34 +140,33 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(const uint16_t* __restr
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
-  double acc[EB][TB] = {};
+  Sum2 acc[EB][TB];
   for (int32_t k = 8 * threadIdx.x; k < H; k += 2048) {
-    float w[EB][8], x[TB][8];
+    float w[EB][8];
+    uint4 raw[TB];
 #pragma unroll
     for (int i = 0; i < EB; ++i) RouterRow<RT>::template load<Vec>(router, min(e0 + i, E - 1), k, H, w[i]);
     // rows are padded to 8 values, and the router's values behind H are zeros
 #pragma unroll
-    for (int j = 0; j < TB; ++j) unpack8<T>(load_act8<true>(X + min(t0 + j, tokens - 1) * ldx, k, H), x[j]);
+    for (int j = 0; j < TB; ++j) raw[j] = load_act8<true>(X + min(t0 + j, tokens - 1) * ldx, k, H);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      double wd[EB], xd[TB];
-#pragma unroll
-      for (int i = 0; i < EB; ++i) wd[i] = w[i][c];
-#pragma unroll
-      for (int j = 0; j < TB; ++j) xd[j] = x[j][c];
+    for (int j = 0; j < TB; ++j) {
+      float x[8];
+      unpack8<T>(raw[j], x);
 #pragma unroll
       for (int i = 0; i < EB; ++i)
 #pragma unroll
-        for (int j = 0; j < TB; ++j) acc[i][j] = fma(wd[i], xd[j], acc[i][j]);
+        for (int c = 0; c < 8; ++c) add_product<RT>(acc[i][j], w[i][c], x[c]);
     }
   }
 #pragma unroll
   for (int i = 0; i < EB; ++i)
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
+      double v = acc[i][j].value();
 #pragma unroll
-      for (int m = 16; m > 0; m >>= 1) acc[i][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[i][j], m);
-      if (lane == 0) part[warp][i * TB + j] = acc[i][j];
+      for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+      if (lane == 0) part[warp][i * TB + j] = v;
     }
   __syncthreads();
   if (threadIdx.x < EB * TB) {
@@ -178,7 +202,7 @@ __device__ __forceinline__ void top_k_of(const double* logits, int32_t E, int32_
 #pragma unroll
   for (int i = 0; i < Per; ++i) {
     const int32_t e = lane + 32 * i;
-    const double v = e < E ? logits[e] : 0.0;
+    const double v = e < E ? __ldcg(logits + e) : 0.0;
     nan |= v != v;
     key[i] = e < E ? max(sort_key(v), 1ull) : 0ull;
   }
@@ -246,28 +270,102 @@ __device__ __forceinline__ uint32_t in_first_cta(const void* p) {
   return a;
 }
 
+// The logits of a small layer by a cluster: CTA `rank` has every eighth expert,
+// and `ways` of its warps share an expert's columns.
+template <typename T, typename RT, bool Vec, int TB>
+__device__ __forceinline__ void small_logits(const uint16_t* X, int64_t ldx, const void* router, int32_t H,
+                                             int32_t tokens, int32_t E, int rank,
+                                             double (&part)[kRouteWarps][kMoeMaxTokens], double* logits) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t mine = (E - rank + kRouteCtas - 1) / kRouteCtas;
+  int ways = kRouteWarps;
+  while (ways > 1 && kRouteWarps / ways < mine) ways /= 2;
+  const int at_once = kRouteWarps / ways;
+  for (int32_t base = 0; base < mine; base += at_once) {
+    const int32_t i = base + warp / ways, e = rank + kRouteCtas * i;
+    for (int32_t t0 = 0; t0 < tokens && i < mine; t0 += TB) {
+      Sum2 acc[TB];
+#pragma unroll(TB == 1 ? 4 : 2)
+      for (int32_t k = 8 * (lane + 32 * (warp % ways)); k < H; k += 256 * ways) {
+        float w[8];
+        uint4 raw[TB];
+        RouterRow<RT>::template load<Vec>(router, e, k, H, w);
+#pragma unroll
+        for (int j = 0; j < TB; ++j) raw[j] = load_act8<true>(X + min(t0 + j, tokens - 1) * ldx, k, H);
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+          float x[8];
+          unpack8<T>(raw[j], x);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) add_product<RT>(acc[j], w[c], x[c]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TB; ++j) {
+        double v = acc[j].value();
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+        if (lane == 0) part[warp][min(t0 + j, tokens - 1)] = v;
+      }
+    }
+    __syncthreads();
+    for (int32_t o = threadIdx.x; o < at_once * tokens; o += kRouteThreads) {
+      const int32_t j = o / tokens, t = o - j * tokens;
+      if (base + j >= mine) continue;
+      double sum = 0.0;
+      for (int w = 0; w < ways; ++w) sum += part[j * ways + w][t];
+      logits[static_cast<int64_t>(t) * E + rank + kRouteCtas * (base + j)] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+struct RouteParams {
+  bool given;          // ids and weights are inputs
+  const uint16_t* X;   // a small layer's activations, whose logits are made here; else nullptr
+  int64_t ldx;
+  const void* router;
+  int32_t H, tokens, E, top_k;
+  bool renormalize, router_f32, router_vec;
+  int32_t* ids;
+  float* weights;
+};
+
 // A cluster: a warp per token chooses (or takes the caller's choice) and sets
 // the token's bit in its experts' sets, which the first CTA holds; then that
 // CTA makes the running experts' lists: their sizes' running sum, and a pair's
 // place in its list from the bits below its own.  An id outside 0 .. E - 1
 // contributes nothing; one that a token names twice runs once with the sum of
 // its weights.
-template <int Per>
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(bool given, int32_t tokens, int32_t E, int32_t top_k,
-                                                                  bool renormalize, int32_t* ids, float* weights,
-                                                                  Workspace ws) {
+template <typename T, int Per>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p, Workspace ws) {
   __shared__ unsigned long long mask[kMoeMaxExperts];
   __shared__ int32_t start[kMoeMaxExperts];
   __shared__ int32_t part[kRouteWarps][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t tokens = p.tokens, E = p.E, top_k = p.top_k;
+  int32_t* ids = p.ids;
+  float* weights = p.weights;
   const uint32_t rank = cluster_rank();
   mask[tid] = 0;
   griddep_wait();
   griddep_launch_dependents();
+  if (p.X) {
+    __shared__ double sums[kRouteWarps][kMoeMaxTokens];
+#define FLASHSPMM_SMALL(RT, VEC)                                                                                   \
+  tokens == 1 ? small_logits<T, RT, VEC, 1>(p.X, p.ldx, p.router, p.H, tokens, E, rank, sums, ws.logits) \
+              : small_logits<T, RT, VEC, 2>(p.X, p.ldx, p.router, p.H, tokens, E, rank, sums, ws.logits)
+    if (p.router_f32)
+      p.router_vec ? (FLASHSPMM_SMALL(float, true)) : (FLASHSPMM_SMALL(float, false));
+    else
+      p.router_vec ? (FLASHSPMM_SMALL(T, true)) : (FLASHSPMM_SMALL(T, false));
+#undef FLASHSPMM_SMALL
+    __threadfence();
+  }
   cluster_sync();
   for (int32_t t = rank + kRouteCtas * warp; t < tokens; t += kRouteCtas * kRouteWarps) {
-    if (!given)
-      top_k_of<Per>(ws.logits + static_cast<int64_t>(t) * E, E, top_k, renormalize, lane, ids + t * top_k,
+    if (!p.given)
+      top_k_of<Per>(ws.logits + static_cast<int64_t>(t) * E, E, top_k, p.renormalize, lane, ids + t * top_k,
                     weights + t * top_k);
     __syncwarp();
     if (lane < top_k) {
@@ -303,7 +401,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(bool given, in
   }
   start[tid] = first - count;
   if (tid == kRouteThreads - 1) *ws.running = slot;
-  if (runs) ws.slots[slot - 1] = Slot{tid, first - count, count, 0};
+  if (runs) ws.slots[slot - 1] = Slot{tid, first - count, count, static_cast<uint32_t>(mask[tid])};
   __syncthreads();
   for (int32_t i = tid; i < tokens * top_k; i += kRouteThreads) {
     const int32_t t = i / top_k, e = __ldcg(ids + i);
@@ -339,6 +437,7 @@ struct ExpertParams {
   const uint16_t* X;
   int64_t ldx;
   int32_t H;             // columns of X that may be read
+  int32_t tokens;
   int32_t activation;
   int32_t pairs;         // of strips a CTA takes
   uint32_t shared;
@@ -409,6 +508,95 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
   }
 }
 
+// Up to eight tokens: a CTA has one strip of the output and all running
+// experts, whose units its warps share in runs.  A token is a column of the
+// product (zeros where the expert is not its choice), so a warp adds an expert's
+// weighted sums in registers and the CTA its warps', and no partial result
+// leaves the SM.
+constexpr int kDirectWarps = 16, kDirectTokens = 8, kDirectSlots = kDirectTokens * kMoeMaxTopK;
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(const ExpertParams p,
+                                                                               T* __restrict__ out, int64_t ldo) {
+  constexpr int kAhead = 2;
+  __shared__ Slot slots[kDirectSlots];
+  __shared__ float weight[kDirectSlots][kDirectTokens];
+  __shared__ float red[kDirectWarps][kDirectTokens][20];  // 16 rows, and the fragments' stores meet all banks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  griddep_wait();
+  const int32_t running = *p.ws.running, units = p.down.units, strip = blockIdx.x;
+  for (int i = threadIdx.x; i < running * kDirectTokens; i += kDirectWarps * 32) {
+    const Slot s = p.ws.slots[i >> 3];
+    const int n = i & 7;
+    if (n == 0) slots[i >> 3] = s;
+    weight[i >> 3][n] =
+        s.tokens >> n & 1 ? p.ws.pair_weight[s.first + __popc(s.tokens & ((1u << n) - 1))] : 0.0f;
+  }
+  __syncthreads();
+  const int64_t items = static_cast<int64_t>(running) * units;
+  const int32_t from = static_cast<int32_t>(items * warp / kDirectWarps);
+  const int32_t to = static_cast<int32_t>(items * (warp + 1) / kDirectWarps);
+  const W4Dev& A = p.down;
+  int32_t s_load = from / units, u_load = from - s_load * units;  // of the next record to be read
+  const auto load = [&](StripUnit<T, NG>& unit) {
+    unit.load(A.at(A.unit(slots[s_load].expert, strip, u_load)), lane, A.zeros);
+    if (++u_load == units) {
+      u_load = 0;
+      ++s_load;
+    }
+  };
+  StripUnit<T, NG> buf[kAhead][1];
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d)
+    if (from + d < to) load(buf[d][0]);
+  int32_t s = from / units, u = from - s * units;
+  float total[4] = {}, acc[1][1][4] = {};
+  const uint16_t* row = nullptr;
+  bool fresh = true;
+  for (int32_t base = from; base < to; base += kAhead) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int32_t i = base + d;
+      if (i >= to) break;
+      if (fresh) {
+        const uint32_t tokens = slots[s].tokens;
+        row = tokens >> g & 1 ? p.ws.h + (slots[s].first + __popc(tokens & ((1u << g) - 1))) * p.ws.ldh + 8 * t : nullptr;
+        fresh = false;
+      }
+      uint4 x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        x[b] = make_uint4(0, 0, 0, 0);
+        if (row && u * kW4UnitCols + 32 * b + 8 * t < p.ws.ldh)
+          x[b] = *reinterpret_cast<const uint4*>(row + u * kW4UnitCols + 32 * b);
+      }
+      strip_unit<T, NG, 1, 1, 1>(buf[d], 1, [&](int, int b) { return x[b]; }, acc);
+      if (i + kAhead < to) load(buf[d][0]);
+      if (++u == units || i + 1 == to) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          total[k] = fmaf(weight[s][2 * t + (k & 1)], acc[0][0][k], total[k]);
+          acc[0][0][k] = 0.0f;
+        }
+        u = 0;
+        ++s;
+        fresh = true;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) red[warp][2 * t + (k & 1)][g + 8 * (k >> 1)] = total[k];
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int n = threadIdx.x >> 4, r = threadIdx.x & 15;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDirectWarps; ++w) sum += red[w][n][r];
+    const int32_t m = strip * 16 + r;
+    if (n < p.tokens && m < A.M) out[n * ldo + m] = from_float<T>(sum);
+  }
+}
+
 // out[token] = the sum of its pairs' y, in the order of its choice.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_join_kernel(const float* __restrict__ y, const int32_t* __restrict__ place,
@@ -476,6 +664,9 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
   e = launch_after(gate_up, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
                    1, s, p);
   if (e != cudaSuccess) return e;
+  if (c.tokens <= kDirectTokens)
+    return launch_after(moe_down_direct_kernel<T, NG>, dim3(p.down.strips), kDirectWarps * 32, 0, 1, s, p,
+                        static_cast<T*>(c.out), c.ldo);
   all = (p.down.strips + 1) / 2;
   p.pairs = pairs_per_cta(running, all, p.down.units, pairs / running);
   p.shared = strip_shared(rows, p.down.units, NT);
@@ -505,16 +696,31 @@ cudaError_t logits_as(const MoeCall& c, const ExpertParams& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t layer_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
-  const int32_t E = c.gate.count;
+  const int32_t E = c.gate.count, H = c.gate.K;
+  // One cluster makes the logits of a small layer itself; a larger one has a kernel for them.
+  const bool small = static_cast<int64_t>(c.tokens) * E * H <= (2 << 20);
+  RouteParams r{};
+  r.given = c.router == nullptr;
+  r.X = c.router && small ? p.X : nullptr;
+  r.ldx = p.ldx;
+  r.router = c.router;
+  r.H = H;
+  r.tokens = c.tokens;
+  r.E = E;
+  r.top_k = c.top_k;
+  r.renormalize = c.renormalize;
+  r.router_f32 = c.router_dtype == FLASHSPMM_F32;
+  r.router_vec = (reinterpret_cast<uintptr_t>(c.router) & 15u) == 0 && H % 8 == 0;
+  r.ids = c.ids;
+  r.weights = c.weights;
   cudaError_t e = cudaSuccess;
-  if (c.router) e = c.router_dtype == FLASHSPMM_F32 ? logits_as<T, float>(c, p, s) : logits_as<T, T>(c, p, s);
+  if (c.router && !small) e = r.router_f32 ? logits_as<T, float>(c, p, s) : logits_as<T, T>(c, p, s);
   if (e != cudaSuccess) return e;
-  auto route = E <= 64 ? moe_route_kernel<2> : E <= 128 ? moe_route_kernel<4> : moe_route_kernel<16>;
-  e = launch_after(route, dim3(kRouteCtas), kRouteThreads, 0, kRouteCtas, s, c.router == nullptr, c.tokens, E, c.top_k,
-                   c.renormalize, c.ids, c.weights, p.ws);
+  auto route = E <= 64 ? moe_route_kernel<T, 2> : E <= 128 ? moe_route_kernel<T, 4> : moe_route_kernel<T, 16>;
+  e = launch_after(route, dim3(kRouteCtas), kRouteThreads, 0, kRouteCtas, s, r, p.ws);
   if (e != cudaSuccess) return e;
-  // Tokens that an expert's codes serve at a time: 8, 16 or 32.  An expert with more reads its codes again, so
-  // 32, which leave an SM half as many warps, are for experts that get more than 12 on average.
+  // Tokens that an expert's codes serve at a time: 8, 16 or 32.  An expert with more reads its codes again; 32
+  // leave an SM half as many warps, and are for experts that get more than 12 on average.
   const bool many = static_cast<int64_t>(c.tokens) * c.top_k > 12 * static_cast<int64_t>(E);
 #define FLASHSPMM_EXPERTS(NG)                                  \
   c.tokens <= 8             ? experts_as<T, NG, 1>(c, p, s)    \
@@ -543,6 +749,7 @@ cudaError_t launch_moe_w4(const MoeCall& c, void* workspace, cudaStream_t s) {
   p.X = static_cast<const uint16_t*>(c.X);
   p.ldx = c.ldx;
   p.H = static_cast<int32_t>(aligned_k(H));  // the aligned copy is padded with zeros
+  p.tokens = c.tokens;
   p.activation = c.activation;
   if (!aligned) {
     const cudaError_t e = launch_align_rows(c.X, c.ldx, c.tokens, H, p.ws.x, s);

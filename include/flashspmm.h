@@ -413,8 +413,8 @@ flashspmm_status flashspmm_w4_decode(const flashspmm_w4* A, void* W, int32_t w_d
 size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B, int64_t ldb, int32_t N);
 
 /* Skinny product C = A x B with fp32 sums.  Up to N = 8 the sums are of s times
- * whole numbers q - z; above, a weight s * (q - z) is rounded to A->dtype first,
- * as flashspmm_w4_decode gives it.
+ * whole numbers q - z; above, a weight s * (q - z) may be rounded to A->dtype
+ * first, as flashspmm_w4_decode gives it.
  *   A          a view with count = 1.
  *   B          device, A->dtype, N rows of K activations, ldb values apart
  *              (any alignment; rows that start on 16 bytes with K % 8 == 0 are
@@ -449,9 +449,9 @@ size_t flashspmm_moe_w4_workspace_bytes(const flashspmm_w4* gate, const void* X,
  *   X          device, dtype, `tokens` rows of H, ldx values apart (alignment
  *              as in flashspmm_w4_matmul).
  *   router     device, E x H row-major, dtype or FLASHSPMM_F32 (router_dtype).
- *              Logits are summed in 64 bits, so the choice does not depend on
- *              the order of a sum.  A NaN logit is chosen last and its token's
- *              p are NaN.
+ *              Logits are summed in some 46 bits, so the choice does not depend
+ *              on the order of a sum.  A NaN logit is chosen last and its
+ *              token's p are NaN.
  *              NULL: ids and weights are inputs, a routing of the caller's.
  *              An id outside 0 .. E - 1 contributes nothing, one named twice
  *              by a token counts with the sum of its weights.

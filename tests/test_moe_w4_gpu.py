@@ -79,7 +79,8 @@ def check(got, want, bound, what=""):
 
 @pytest.mark.parametrize("T,E,k,H,F", [(1, 4, 1, 128, 128), (1, 8, 2, 264, 200), (3, 5, 5, 130, 77), (8, 16, 4, 256, 136),
                                        (9, 3, 2, 512, 40), (17, 8, 2, 200, 264), (40, 12, 3, 136, 128),
-                                       (64, 2, 1, 128, 72), (64, 40, 8, 96, 64), (2, 512, 16, 64, 32)])
+                                       (64, 2, 1, 128, 72), (64, 40, 8, 96, 64), (2, 512, 16, 64, 32),
+                                       (8, 16, 16, 128, 136), (33, 3, 3, 640, 520), (64, 4, 4, 1024, 264)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_layer(T, E, k, H, F, dtype):
     group = (32, 64, 128)[(T + k) % 3]
@@ -238,6 +239,43 @@ def test_refusals():
             bad()
         assert e.value.status == status
     assert fs.moe_w4(X[:0], router, *packed, 1)[0].shape == (0, H)
+
+
+def test_workspace_is_checked():
+    from unstructured_sparse_skinny_b200 import binding
+    lib = binding.load_library()
+    E, H, F, T = 4, 128, 64, 3
+    _, (gate, up, down) = layer(E, H, F, 64, torch.float16)
+    X = torch.ones((T, H), device="cuda", dtype=torch.float16)
+    ids, weights = torch.zeros((T, 1), device="cuda", dtype=torch.int32), torch.ones((T, 1), device="cuda")
+    out = torch.full((T, H), 5.0, device="cuda", dtype=torch.float16)
+    need = lib.flashspmm_moe_w4_workspace_bytes(gate._ref, X.data_ptr(), H, T, 1)
+    ws = torch.empty(need + 16, device="cuda", dtype=torch.uint8)
+
+    def call(ptr, size):
+        return lib.flashspmm_moe_w4(gate._ref, up._ref, down._ref, X.data_ptr(), H, None, 0, T, 1, 1, 0, ids.data_ptr(),
+                                    weights.data_ptr(), out.data_ptr(), H, ptr, size,
+                                    torch.cuda.current_stream().cuda_stream)
+
+    assert call(None, need) == 4 and call(ws.data_ptr(), need - 1) == 4 and call(ws.data_ptr() + 8, need) == 3
+    torch.cuda.synchronize()
+    assert (out == 5).all()
+    assert call(ws.data_ptr(), need) == 0
+    assert torch.equal(out, fs.moe_w4_experts(X, ids, weights, gate, up, down))
+
+
+@pytest.mark.parametrize("T,E,k,H", [(64, 128, 8, 640), (33, 300, 4, 1024), (5, 64, 3, 8192), (8, 130, 6, 2056)])
+def test_wide_routing(T, E, k, H):
+    """Logits by their own kernel and by the routing cluster, at sizes that split over warps and CTAs."""
+    _, packed = layer(E, H, 16, 128, torch.bfloat16, symmetric=True)
+    X = torch.randn((T, H), device="cuda", generator=gen(1)).bfloat16()
+    router = torch.randn((E, H), device="cuda", generator=gen(2)) * H ** -0.5
+    for r in (router, router.bfloat16()):
+        for renormalize in (True, False):
+            _, ids, weights = fs.moe_w4(X, r, *packed, k, renormalize=renormalize)
+            want_ids, want_weights = route64(X, r, k, renormalize)
+            assert torch.equal(ids.long(), want_ids)
+            assert torch.allclose(weights.double(), want_weights, rtol=2e-6, atol=0)
 
 
 @pytest.mark.parametrize("T", [1, 20])

@@ -175,7 +175,7 @@ def test_matmul(dtype, group, symmetric, N):
 
 @pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 129, 3), (15, 7, 8), (16, 128, 1), (17, 8, 256), (129, 257, 17),
                                    (4099, 5003, 17), (128, 36864, 5), (20000, 640, 256), (1280, 24576, 256),
-                                   (1280, 24576, 200), (20000, 640, 144), (2600, 24576, 24), (320, 49152, 70), (9216, 64, 1), (2048, 2048, 40)])
+                                   (1280, 24576, 200), (20000, 640, 144), (2600, 24576, 24), (8192, 8192, 12), (300, 300, 250), (320, 49152, 70), (9216, 64, 1), (2048, 2048, 40)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_matmul_whole_numbers_are_exact(M, K, N, dtype):
     codes, scales, zeros = codes_of((M, K), 64, dtype, False, 7, whole=True)
@@ -231,6 +231,29 @@ def test_matmul_non_finite_activations_stay_in_their_row(N):
     assert (got[1] == float("inf")).all()
     B[1, 5] = float("nan")
     assert torch.isnan(fs.w4_matmul(A, B)[1]).all()
+
+
+@pytest.mark.parametrize("N,K", [(3, 131), (200, 4096)])
+def test_matmul_checks_its_workspace(N, K):
+    """Too small, missing or misaligned scratch is refused and nothing is written."""
+    from unstructured_sparse_skinny_b200 import binding
+    lib = binding.load_library()
+    A = fs.w4_pack(*codes_of((2048, K), 128, torch.float16, True, 2))
+    B = torch.ones((N, K), device="cuda", dtype=torch.float16)
+    C = torch.full((N, 2048), 5.0, device="cuda", dtype=torch.float16)
+    need = lib.flashspmm_w4_matmul_workspace_bytes(A._ref, B.data_ptr(), K, N)
+    assert need > 0
+    ws = torch.empty(need + 16, device="cuda", dtype=torch.uint8)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(ptr, size):
+        return lib.flashspmm_w4_matmul(A._ref, B.data_ptr(), K, C.data_ptr(), 2048, 0, N, ptr, size, stream)
+
+    assert call(None, need) == 4 and call(ws.data_ptr(), need - 1) == 4 and call(ws.data_ptr() + 8, need) == 3
+    torch.cuda.synchronize()
+    assert (C == 5).all()
+    assert call(ws.data_ptr(), need) == 0
+    assert torch.equal(C, fs.w4_matmul(A, B))
 
 
 def test_matmul_empty():

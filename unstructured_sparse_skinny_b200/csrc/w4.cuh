@@ -342,12 +342,11 @@ inline int64_t aligned_k(int32_t K) { return (static_cast<int64_t>(K) + 7) / 8 *
 bool rows_aligned(const void* X, int64_t ld, int32_t K);
 cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K, void* out, cudaStream_t s);
 
-size_t w4_matmul_workspace(int32_t M, int32_t K, int32_t N, bool aligned);
+size_t w4_matmul_workspace(const flashspmm_w4* A, int32_t N, bool aligned);
 cudaError_t launch_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                              int32_t N, void* workspace, cudaStream_t s);
 
-// The same product by tcgen05 (w4_gemm.cu), for N > kW4FragmentTokens.
-constexpr int kW4FragmentTokens = 8;
+// The same product by tcgen05 (w4_gemm.cu).
 size_t w4_gemm_workspace(int32_t M, int32_t K, int32_t N);
 cudaError_t launch_w4_gemm(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                            int32_t N, void* workspace, cudaStream_t s);

@@ -83,7 +83,7 @@ flashspmm_status flashspmm_w4_decode(const flashspmm_w4* A, void* W, int32_t w_d
 
 size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B, int64_t ldb, int32_t N) {
   if (check_w4(A) != FLASHSPMM_OK || N <= 0 || N > 256 || A->M == 0 || A->K == 0) return 0;
-  return w4_matmul_workspace(A->M, A->K, N, rows_aligned(B, ldb, A->K));
+  return w4_matmul_workspace(A, N, rows_aligned(B, ldb, A->K));
 }
 
 flashspmm_status flashspmm_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc,
@@ -103,7 +103,7 @@ flashspmm_status flashspmm_w4_matmul(const flashspmm_w4* A, const void* B, int64
   if (A->K == 0) return done(cudaMemset2DAsync(C, ldc * width, 0, A->M * width, N, s));
   if (!B) return FLASHSPMM_ERR_INVALID_ARG;
   if (!on2(B)) return FLASHSPMM_ERR_ALIGNMENT;
-  const size_t need = w4_matmul_workspace(A->M, A->K, N, rows_aligned(B, ldb, A->K));
+  const size_t need = w4_matmul_workspace(A, N, rows_aligned(B, ldb, A->K));
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return FLASHSPMM_ERR_CAPACITY;
     if (!aligned16(workspace)) return FLASHSPMM_ERR_ALIGNMENT;

@@ -1,5 +1,5 @@
 // Skinny product with 4-bit weights: C[N][M] = B[N][K] x A[M][K]^T, N <= 256.
-// Up to eight tokens run here, more on tcgen05 (w4_gemm.cu).
+// Few tokens and small products run here, the others on tcgen05 (w4_gemm.cu).
 
 #include "w4_strips.cuh"
 
@@ -18,7 +18,7 @@ struct MatmulParams {
   int32_t N;
 };
 
-// One strip of 16 rows a CTA, up to eight tokens: its warps have the units in
+// One strip of 16 rows and eight tokens a CTA: its warps have the units in
 // turn and add up at the end.  Codes come two units ahead; the activations,
 // which all CTAs read again, from L1 and L2 as the fragments need them.  (Staged
 // in shared memory first, they delay the short-lived CTAs more than they save:
@@ -31,7 +31,8 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
   const uint8_t* strip = p.A.at(p.A.unit(0, blockIdx.x, 0));
   const int32_t pitch = 8 * p.A.record;  // from a strip's unit to its next
   const int32_t units = p.A.units;
-  const uint16_t* row = g < p.N ? p.B + g * p.ldb + 8 * t : nullptr;
+  const int32_t n0 = blockIdx.y * 8;
+  const uint16_t* row = n0 + g < p.N ? p.B + (n0 + g) * p.ldb + 8 * t : nullptr;
   StripUnit<T, NG> buf[kAhead][1];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
@@ -57,10 +58,10 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
   for (int i = 0; i < 4; ++i) red[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[0][0][i];
   __syncthreads();
   if (threadIdx.x < 128) {
-    const int n = threadIdx.x >> 4, r = threadIdx.x & 15;
+    const int i = threadIdx.x >> 4, r = threadIdx.x & 15, n = n0 + i;
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kMatmulWarps; ++w) sum += red[w][n][r];
+    for (int w = 0; w < kMatmulWarps; ++w) sum += red[w][i][r];
     const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + r;
     if (n < p.N && m < p.A.M) {
       if (p.c_f32)
@@ -93,14 +94,26 @@ cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K
   return cudaGetLastError();
 }
 
-size_t w4_matmul_workspace(int32_t M, int32_t K, int32_t N, bool aligned) {
-  if (N > kW4FragmentTokens) return w4_gemm_workspace(M, K, N);
-  return aligned ? 0 : static_cast<size_t>(N) * aligned_k(K) * 2;
+// Eight tokens at a time here, or all at once by tcgen05?  Measured, in us: here
+// 3.5 (6 if the activations have to be copied first) and 0.24 per 1000 records
+// for every eight tokens, 0.3 with groups of 32; there 8.5 (two kernels, the
+// joining of blocks) and 0.3 per 1000 records.
+static bool by_fragments(const flashspmm_w4* A, int32_t N, bool aligned) {
+  if (N <= 8) return true;
+  const double records = 8e-3 * w4_blocks(A->M) * w4_units(A->K);
+  const double each = A->group == 32 ? 0.3 : 0.24;
+  return (aligned ? 3.5 : 6.0) + each * ((N + 7) / 8) * records < 8.5 + 0.3 * records;
+}
+
+size_t w4_matmul_workspace(const flashspmm_w4* A, int32_t N, bool aligned) {
+  if (!by_fragments(A, N, aligned)) return w4_gemm_workspace(A->M, A->K, N);
+  return aligned ? 0 : static_cast<size_t>(N) * aligned_k(A->K) * 2;
 }
 
 cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                              int32_t N, void* workspace, cudaStream_t s) {
-  if (N > kW4FragmentTokens) return launch_w4_gemm(in, B, ldb, C, ldc, c_f32, N, workspace, s);
+  if (!by_fragments(in, N, rows_aligned(B, ldb, in->K)))
+    return launch_w4_gemm(in, B, ldb, C, ldc, c_f32, N, workspace, s);
   MatmulParams p{};
   p.A = w4_dev(in);
   if (!rows_aligned(B, ldb, p.A.K)) {
@@ -116,10 +129,11 @@ cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb,
   p.ldc = ldc;
   p.c_f32 = c_f32;
   p.N = N;
+  const dim3 grid(p.A.strips, (N + 7) / 8);
 #define FLASHSPMM_BY_GROUP(T)                                                                \
-  p.A.group == 128  ? w4_matmul_kernel<T, 1><<<p.A.strips, kMatmulWarps * 32, 0, s>>>(p)         \
-  : p.A.group == 64 ? w4_matmul_kernel<T, 2><<<p.A.strips, kMatmulWarps * 32, 0, s>>>(p)         \
-                    : w4_matmul_kernel<T, 4><<<p.A.strips, kMatmulWarps * 32, 0, s>>>(p)
+  p.A.group == 128  ? w4_matmul_kernel<T, 1><<<grid, kMatmulWarps * 32, 0, s>>>(p)         \
+  : p.A.group == 64 ? w4_matmul_kernel<T, 2><<<grid, kMatmulWarps * 32, 0, s>>>(p)         \
+                    : w4_matmul_kernel<T, 4><<<grid, kMatmulWarps * 32, 0, s>>>(p)
   if (in->dtype == FLASHSPMM_F16)
     FLASHSPMM_BY_GROUP(__half);
   else

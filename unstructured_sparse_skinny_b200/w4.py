@@ -96,8 +96,8 @@ def _raw_stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _scratch(nbytes: int, device: torch.device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _scratch(nbytes: int, like: torch.Tensor):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def _cuda(t, name: str, dtypes) -> None:
@@ -114,6 +114,8 @@ def _no_grad(*tensors) -> None:
 
 def _rows(t: torch.Tensor) -> tuple:
     """A 2-D tensor with unit stride along its rows, and the distance of its rows."""
+    if t.is_contiguous():
+        return t, t.shape[1]
     if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
         t = t.contiguous()
     return t, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
@@ -222,13 +224,13 @@ def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None
     B, ldb = _rows(B)
     N = B.shape[0]
     if C is None:
-        C, ldc = torch.empty((N, A.M), dtype=dtype, device=device), A.M
+        C, ldc, c_type = B.new_empty((N, A.M)), A.M, _DTYPES[dtype]
     else:
-        ldc = _output(C, (N, A.M), (dtype, torch.float32), device, "C")
+        ldc, c_type = _output(C, (N, A.M), (dtype, torch.float32), device, "C"), _DTYPES[C.dtype]
     ptr = B.data_ptr()
     need = lib.flashspmm_w4_matmul_workspace_bytes(A._ref, ptr, ldb, N)
-    ws = _scratch(need, device)
-    status = lib.flashspmm_w4_matmul(A._ref, ptr, ldb, C.data_ptr(), ldc, _DTYPES[C.dtype], N,
+    ws = _scratch(need, B)
+    status = lib.flashspmm_w4_matmul(A._ref, ptr, ldb, C.data_ptr(), ldc, c_type, N,
                                      None if ws is None else ws.data_ptr(), need, _raw_stream(device))
     if status:
         binding._check(status, "w4_matmul")
@@ -241,12 +243,12 @@ def _moe(X, router, gate, up, down, top_k, renormalize, activation, ids, weights
     X, ldx = _rows(X)
     T = X.shape[0]
     if out is None:
-        out, ldo = torch.empty((T, gate.K), dtype=dtype, device=device), gate.K
+        out, ldo = X.new_empty((T, gate.K)), gate.K
     else:
         ldo = _output(out, (T, gate.K), (dtype, ), device, "out")
     ptr = X.data_ptr()
     need = lib.flashspmm_moe_w4_workspace_bytes(gate._ref, ptr, ldx, T, top_k)
-    ws = _scratch(need, device)
+    ws = _scratch(need, X)
     status = lib.flashspmm_moe_w4(
         gate._ref, None if up is None else up._ref, down._ref, ptr, ldx, None if router is None else router.data_ptr(),
         _DTYPES[dtype if router is None else router.dtype], T, top_k, renormalize, activation, ids.data_ptr(),
@@ -289,8 +291,8 @@ def moe_w4(X: torch.Tensor, router: torch.Tensor, gate: W4, up: W4 | None, down:
         with _On(device, stream):
             return moe_w4(X, router, gate, up, down, top_k, renormalize, activation, out)
     _no_grad(X, router)
-    ids = torch.empty((X.shape[0], top_k), dtype=torch.int32, device=device)
-    weights = torch.empty((X.shape[0], top_k), dtype=torch.float32, device=device)
+    ids = X.new_empty((X.shape[0], top_k), dtype=torch.int32)
+    weights = X.new_empty((X.shape[0], top_k), dtype=torch.float32)
     out = _moe(X, router.contiguous(), gate, up, down, top_k, int(renormalize), _ACTIVATIONS[activation], ids, weights,
                out)
     return out, ids, weights

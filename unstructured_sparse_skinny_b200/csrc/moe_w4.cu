@@ -22,6 +22,7 @@ namespace {
 constexpr int kRouteWarps = 16;
 constexpr int kRouteThreads = kRouteWarps * 32;
 constexpr int kRouteCtas = 8;  // one cluster
+constexpr int kDirectTokens = 8;  // see moe_down_direct_kernel
 
 // An expert that runs: its tokens are pairs [first, first + count), and their
 // bits among the first 32 tokens.
@@ -37,7 +38,7 @@ struct Workspace {
   float* pair_weight;
   int32_t* place;        // [T][top_k]: the pair of a token's j-th expert, -1 where there is none
   double* logits;        // [T][E]
-  uint16_t* h;           // [T * top_k][ldh]
+  uint16_t* h;           // [T * top_k][ldh]; up to eight tokens what its rounding left follows
   float* y;              // [T * top_k][H], weighted
   uint16_t* x;           // aligned copy of the activations, if one is needed
   int64_t ldh;
@@ -62,7 +63,7 @@ Workspace carve(void* base, int32_t T, int32_t E, int32_t top_k, int32_t H, int3
   w.pair_weight = reinterpret_cast<float*>(take(4 * pairs));
   w.place = reinterpret_cast<int32_t*>(take(4 * pairs));
   w.logits = reinterpret_cast<double*>(take(sizeof(double) * T * E));
-  w.h = reinterpret_cast<uint16_t*>(take(2 * pairs * w.ldh));
+  w.h = reinterpret_cast<uint16_t*>(take(2 * pairs * w.ldh * (T <= kDirectTokens ? 2 : 1)));
   w.y = reinterpret_cast<float*>(take(sizeof(float) * pairs * H));
   w.x = reinterpret_cast<uint16_t*>(take(aligned ? 0 : static_cast<size_t>(T) * aligned_k(H) * 2));
   w.bytes = o;
@@ -439,13 +440,16 @@ struct ExpertParams {
   int32_t H;             // columns of X that may be read
   int32_t tokens;
   int32_t activation;
+  int64_t rest;          // from an h to what its rounding left, in values
   int32_t pairs;         // of strips a CTA takes
   uint32_t shared;
   Workspace ws;
 };
 
 // h[pair][f] for some strips of 16 rows f of a running expert.  h is rounded
-// to the activations' type: it is the next product's tensor-core operand.
+// to the activations' type: it is the next product's tensor-core operand.  Up to
+// eight tokens, where a few large h carry an output and a rounding of each shows,
+// what the rounding leaves is kept too, rounded likewise.
 template <typename T, int NG, int NT, bool Gated>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -468,8 +472,14 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
         at, A.units, p.H, rows, p.pairs, smem, p.shared, [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
     const auto store = [&](int32_t n, int32_t f, float v) {
       // columns behind F pad h to 16 bytes: finite whatever x holds
-      if (f < p.ws.ldh)
-        reinterpret_cast<T*>(p.ws.h)[(slot.first + n0 + n) * p.ws.ldh + f] = from_float<T>(f < A.M ? v : 0.0f);
+      if (f >= p.ws.ldh) return;
+      T* h = reinterpret_cast<T*>(p.ws.h) + (slot.first + n0 + n) * p.ws.ldh + f;
+      const T rounded = from_float<T>(f < A.M ? v : 0.0f);
+      *h = rounded;
+      if (p.tokens <= kDirectTokens) {
+        const float left = f < A.M ? v - to_float(rounded) : 0.0f;
+        h[p.rest] = from_float<T>(isfinite(left) ? left : 0.0f);  // of an h that rounds to infinity: nothing
+      }
     };
     strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t f = (pair0 + i) * (Gated ? 16 : 32) + row;
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
 // product (zeros where the expert is not its choice), so a warp adds an expert's
 // weighted sums in registers and the CTA its warps', and no partial result
 // leaves the SM.
-constexpr int kDirectWarps = 16, kDirectTokens = 8, kDirectSlots = kDirectTokens * kMoeMaxTopK;
+constexpr int kDirectWarps = 12, kDirectSlots = kDirectTokens * kMoeMaxTopK;
 
 template <typename T, int NG>
 __global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(const ExpertParams p,
@@ -563,14 +573,16 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(c
         row = tokens >> g & 1 ? p.ws.h + (slots[s].first + __popc(tokens & ((1u << g) - 1))) * p.ws.ldh + 8 * t : nullptr;
         fresh = false;
       }
-      uint4 x[4];
+      uint4 x[4][2];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        x[b] = make_uint4(0, 0, 0, 0);
-        if (row && u * kW4UnitCols + 32 * b + 8 * t < p.ws.ldh)
-          x[b] = *reinterpret_cast<const uint4*>(row + u * kW4UnitCols + 32 * b);
+        x[b][0] = x[b][1] = make_uint4(0, 0, 0, 0);
+        if (row && u * kW4UnitCols + 32 * b + 8 * t < p.ws.ldh) {
+          x[b][0] = *reinterpret_cast<const uint4*>(row + u * kW4UnitCols + 32 * b);
+          x[b][1] = *reinterpret_cast<const uint4*>(row + p.rest + u * kW4UnitCols + 32 * b);
+        }
       }
-      strip_unit<T, NG, 1, 1, 1>(buf[d], 1, [&](int, int b) { return x[b]; }, acc);
+      strip_unit<T, NG, 1, 1, 1, 2>(buf[d], 1, [&](int, int b, int part) { return x[b][part]; }, acc);
       if (i + kAhead < to) load(buf[d][0]);
       if (++u == units || i + 1 == to) {
 #pragma unroll
@@ -750,6 +762,7 @@ cudaError_t launch_moe_w4(const MoeCall& c, void* workspace, cudaStream_t s) {
   p.ldx = c.ldx;
   p.H = static_cast<int32_t>(aligned_k(H));  // the aligned copy is padded with zeros
   p.tokens = c.tokens;
+  p.rest = static_cast<int64_t>(c.tokens) * c.top_k * p.ws.ldh;
   p.activation = c.activation;
   if (!aligned) {
     const cudaError_t e = launch_align_rows(c.X, c.ldx, c.tokens, H, p.ws.x, s);

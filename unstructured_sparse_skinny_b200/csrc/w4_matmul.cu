@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
         x[b] = make_uint4(0, 0, 0, 0);
         if (row && u * 128 + 32 * b + 8 * t < p.A.K) x[b] = __ldg(reinterpret_cast<const uint4*>(row + u * 128 + 32 * b));
       }
-      strip_unit<T, NG, 1, 1, 1>(buf[d], 1, [&](int, int b) { return x[b]; }, acc);
+      strip_unit<T, NG, 1, 1, 1>(buf[d], 1, [&](int, int b, int) { return x[b]; }, acc);
       const int32_t next = u + kAhead * kMatmulWarps;
       if (next < units) buf[d][0].load(strip + static_cast<int64_t>(next) * pitch, lane, p.A.zeros);
     }

@@ -44,9 +44,10 @@ struct StripUnit {
   }
 };
 
-// acc += the unit's product with activations, of R strips; x(nt, b) gives the
-// lane's 16 bytes of its row of tile nt and the unit's 32-column block b.
-template <typename T, int NG, int R, int NT, int Tiles, typename Act>
+// acc += the unit's product with activations, of R strips; x(nt, b, part) gives
+// the lane's 16 bytes of its row of tile nt and the unit's 32-column block b.
+// Activations of several parts are their sum.
+template <typename T, int NG, int R, int NT, int Tiles, int Parts = 1, typename Act>
 __device__ __forceinline__ void strip_unit(const StripUnit<T, NG> (&unit)[R], int tiles, const Act& x,
                                            float (&acc)[R][Tiles][4]) {
   constexpr int kBlocks = 4 / NG;
@@ -66,16 +67,19 @@ __device__ __forceinline__ void strip_unit(const StripUnit<T, NG> (&unit)[R], in
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt > 0 && nt >= tiles) break;
-        const uint4 v = x(nt, blk);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (b == 0)
-            mma16816_zero<T>(d[r][nt], a[r][0], v.x, v.y);
-          else
-            mma16816<T>(d[r][nt], a[r][0], v.x, v.y);
+        for (int part = 0; part < Parts; ++part) {
+          const uint4 v = x(nt, blk, part);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (b == 0 && part == 0)
+              mma16816_zero<T>(d[r][nt], a[r][0], v.x, v.y);
+            else
+              mma16816<T>(d[r][nt], a[r][0], v.x, v.y);
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) mma16816<T>(d[r][nt], a[r][1], v.z, v.w);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) mma16816<T>(d[r][nt], a[r][1], v.z, v.w);
       }
     }
 #pragma unroll
@@ -145,7 +149,7 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
       for (int d = 0; d < kAhead; ++d) {
         if (d == next && u < end) {
           const uint32_t offset = (u - from) * 256;
-          const auto act = [&](int nt, int b) {
+          const auto act = [&](int nt, int b, int) {
             uint4 v;
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)

@@ -462,10 +462,9 @@ size_t flashspmm_moe_w4_workspace_bytes(const flashspmm_w4* gate, const void* X,
  *   tokens     0 .. 64;  E <= 512;  top_k 1 .. 16 (<= E with a router).
  *   workspace  device, 16-byte aligned; needs no initialisation.  Calls that
  *              may run concurrently need separate ones.
- * Products are summed in fp32 and h is rounded to dtype between them (up to eight
- * tokens what the rounding leaves is kept in a second value of dtype; with fp16
- * an h beyond 65504 becomes infinite, as in a layer of separate fp16 calls).
- * Results are deterministic. */
+ * Products are summed in fp32.  Between them h is held in two values of dtype,
+ * its rounding and what that leaves (with fp16 an h beyond 65504 becomes
+ * infinite, as in a layer of separate fp16 calls).  Results are deterministic. */
 flashspmm_status flashspmm_moe_w4(const flashspmm_w4* gate, const flashspmm_w4* up, const flashspmm_w4* down,
                                   const void* X, int64_t ldx, const void* router, int32_t router_dtype, int32_t tokens,
                                   int32_t top_k, int32_t renormalize, int32_t activation, int32_t* ids, float* weights,

@@ -38,7 +38,7 @@ struct Workspace {
   float* pair_weight;
   int32_t* place;        // [T][top_k]: the pair of a token's j-th expert, -1 where there is none
   double* logits;        // [T][E]
-  uint16_t* h;           // [T * top_k][ldh]; up to eight tokens what its rounding left follows
+  uint16_t* h;           // [2][T * top_k][ldh]: rounded, and what the rounding left
   float* y;              // [T * top_k][H], weighted
   uint16_t* x;           // aligned copy of the activations, if one is needed
   int64_t ldh;
@@ -63,7 +63,7 @@ Workspace carve(void* base, int32_t T, int32_t E, int32_t top_k, int32_t H, int3
   w.pair_weight = reinterpret_cast<float*>(take(4 * pairs));
   w.place = reinterpret_cast<int32_t*>(take(4 * pairs));
   w.logits = reinterpret_cast<double*>(take(sizeof(double) * T * E));
-  w.h = reinterpret_cast<uint16_t*>(take(2 * pairs * w.ldh * (T <= kDirectTokens ? 2 : 1)));
+  w.h = reinterpret_cast<uint16_t*>(take(2 * 2 * pairs * w.ldh));
   w.y = reinterpret_cast<float*>(take(sizeof(float) * pairs * H));
   w.x = reinterpret_cast<uint16_t*>(take(aligned ? 0 : static_cast<size_t>(T) * aligned_k(H) * 2));
   w.bytes = o;
@@ -446,10 +446,11 @@ struct ExpertParams {
   Workspace ws;
 };
 
-// h[pair][f] for some strips of 16 rows f of a running expert.  h is rounded
-// to the activations' type: it is the next product's tensor-core operand.  Up to
-// eight tokens, where a few large h carry an output and a rounding of each shows,
-// what the rounding leaves is kept too, rounded likewise.
+// h[pair][f] for some strips of 16 rows f of a running expert.  As the next
+// product's tensor-core operand h is rounded to the activations' type; what the
+// rounding leaves is kept too, rounded likewise, and multiplied beside it.
+// (Without that an output has 1.5 times the error that its own rounding makes: a
+// few large h carry it.  The second products cost a tenth of the layer.)
 template <typename T, int NG, int NT, bool Gated>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -468,18 +469,16 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
   for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
     const int32_t rows = min(slot.count - n0, NT * 8);
     float acc[2][NT][4] = {};
-    strip_product<T, NG, NT>(
+    strip_product<T, NG, NT, 1>(
         at, A.units, p.H, rows, p.pairs, smem, p.shared, [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
     const auto store = [&](int32_t n, int32_t f, float v) {
       // columns behind F pad h to 16 bytes: finite whatever x holds
       if (f >= p.ws.ldh) return;
       T* h = reinterpret_cast<T*>(p.ws.h) + (slot.first + n0 + n) * p.ws.ldh + f;
       const T rounded = from_float<T>(f < A.M ? v : 0.0f);
+      const float left = f < A.M ? v - to_float(rounded) : 0.0f;
       *h = rounded;
-      if (p.tokens <= kDirectTokens) {
-        const float left = f < A.M ? v - to_float(rounded) : 0.0f;
-        h[p.rest] = from_float<T>(isfinite(left) ? left : 0.0f);  // of an h that rounds to infinity: nothing
-      }
+      h[p.rest] = from_float<T>(isfinite(left) ? left : 0.0f);  // of an h that rounds to infinity: nothing
     };
     strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t f = (pair0 + i) * (Gated ? 16 : 32) + row;
@@ -505,9 +504,10 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
   for (int32_t n0 = 0; n0 < slot.count; n0 += NT * 8) {
     const int32_t rows = min(slot.count - n0, NT * 8), first = slot.first + n0;
     float acc[2][NT][4] = {};
-    strip_product<T, NG, NT>(
+    strip_product<T, NG, NT, 2>(
         at, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, p.shared,
-        [&](int32_t n) { return p.ws.h + (first + n) * p.ws.ldh; }, acc);
+        [&](int32_t n) { return p.ws.h + (n < rows ? first + n : first + n - rows) * p.ws.ldh + (n < rows ? 0 : p.rest); },
+        acc);
     strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t m = (pair0 + i) * 32 + row;
       const float w = p.ws.pair_weight[first + n];
@@ -518,23 +518,25 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
   }
 }
 
-// Up to eight tokens: a CTA has one strip of the output and all running
+// Up to eight tokens: a CTA has a pair of strips of the output and all running
 // experts, whose units its warps share in runs.  A token is a column of the
 // product (zeros where the expert is not its choice), so a warp adds an expert's
 // weighted sums in registers and the CTA its warps', and no partial result
 // leaves the SM.
-constexpr int kDirectWarps = 12, kDirectSlots = kDirectTokens * kMoeMaxTopK;
+constexpr int kDirectWarps = 16, kDirectSlots = kDirectTokens * kMoeMaxTopK;
 
 template <typename T, int NG>
-__global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(const ExpertParams p,
+__global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(const ExpertParams p,
                                                                                T* __restrict__ out, int64_t ldo) {
   constexpr int kAhead = 2;
   __shared__ Slot slots[kDirectSlots];
   __shared__ float weight[kDirectSlots][kDirectTokens];
-  __shared__ float red[kDirectWarps][kDirectTokens][20];  // 16 rows, and the fragments' stores meet all banks
+  __shared__ float red[kDirectWarps][kDirectTokens][36];  // 32 rows, and the fragments' stores meet all banks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   griddep_wait();
-  const int32_t running = *p.ws.running, units = p.down.units, strip = blockIdx.x;
+  const int32_t running = *p.ws.running, units = p.down.units;
+  const int32_t strip[2] = {static_cast<int32_t>(2 * blockIdx.x),
+                            min(static_cast<int32_t>(2 * blockIdx.x + 1), p.down.strips - 1)};
   for (int i = threadIdx.x; i < running * kDirectTokens; i += kDirectWarps * 32) {
     const Slot s = p.ws.slots[i >> 3];
     const int n = i & 7;
@@ -548,19 +550,20 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(c
   const int32_t to = static_cast<int32_t>(items * (warp + 1) / kDirectWarps);
   const W4Dev& A = p.down;
   int32_t s_load = from / units, u_load = from - s_load * units;  // of the next record to be read
-  const auto load = [&](StripUnit<T, NG>& unit) {
-    unit.load(A.at(A.unit(slots[s_load].expert, strip, u_load)), lane, A.zeros);
+  const auto load = [&](StripUnit<T, NG> (&unit)[2]) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) unit[r].load(A.at(A.unit(slots[s_load].expert, strip[r], u_load)), lane, A.zeros);
     if (++u_load == units) {
       u_load = 0;
       ++s_load;
     }
   };
-  StripUnit<T, NG> buf[kAhead][1];
+  StripUnit<T, NG> buf[kAhead][2];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
-    if (from + d < to) load(buf[d][0]);
+    if (from + d < to) load(buf[d]);
   int32_t s = from / units, u = from - s * units;
-  float total[4] = {}, acc[1][1][4] = {};
+  float total[2][4] = {}, acc[2][1][4] = {};
   const uint16_t* row = nullptr;
   bool fresh = true;
   for (int32_t base = from; base < to; base += kAhead) {
@@ -582,14 +585,16 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(c
           x[b][1] = *reinterpret_cast<const uint4*>(row + p.rest + u * kW4UnitCols + 32 * b);
         }
       }
-      strip_unit<T, NG, 1, 1, 1, 2>(buf[d], 1, [&](int, int b, int part) { return x[b][part]; }, acc);
-      if (i + kAhead < to) load(buf[d][0]);
+      strip_unit<T, NG, 2, 1, 1, 2>(buf[d], 1, [&](int, int b, int part) { return x[b][part]; }, acc);
+      if (i + kAhead < to) load(buf[d]);
       if (++u == units || i + 1 == to) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          total[k] = fmaf(weight[s][2 * t + (k & 1)], acc[0][0][k], total[k]);
-          acc[0][0][k] = 0.0f;
-        }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            total[r][k] = fmaf(weight[s][2 * t + (k & 1)], acc[r][0][k], total[r][k]);
+            acc[r][0][k] = 0.0f;
+          }
         u = 0;
         ++s;
         fresh = true;
@@ -597,14 +602,16 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 2) moe_down_direct_kernel(c
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) red[warp][2 * t + (k & 1)][g + 8 * (k >> 1)] = total[k];
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) red[warp][2 * t + (k & 1)][16 * r + g + 8 * (k >> 1)] = total[r][k];
   __syncthreads();
-  if (threadIdx.x < 128) {
-    const int n = threadIdx.x >> 4, r = threadIdx.x & 15;
+  if (threadIdx.x < 256) {
+    const int n = threadIdx.x >> 5, r = threadIdx.x & 31;
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kDirectWarps; ++w) sum += red[w][n][r];
-    const int32_t m = strip * 16 + r;
+    const int32_t m = blockIdx.x * 32 + r;
     if (n < p.tokens && m < A.M) out[n * ldo + m] = from_float<T>(sum);
   }
 }
@@ -677,11 +684,11 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
                    1, s, p);
   if (e != cudaSuccess) return e;
   if (c.tokens <= kDirectTokens)
-    return launch_after(moe_down_direct_kernel<T, NG>, dim3(p.down.strips), kDirectWarps * 32, 0, 1, s, p,
+    return launch_after(moe_down_direct_kernel<T, NG>, dim3((p.down.strips + 1) / 2), kDirectWarps * 32, 0, 1, s, p,
                         static_cast<T*>(c.out), c.ldo);
   all = (p.down.strips + 1) / 2;
-  p.pairs = pairs_per_cta(running, all, p.down.units, pairs / running);
-  p.shared = strip_shared(rows, p.down.units, NT);
+  p.pairs = pairs_per_cta(running, all, p.down.units, 2 * pairs / running);
+  p.shared = strip_shared(2 * rows, p.down.units, NT);
   e = launch_after(down, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared, 1,
                    s, p);
   if (e != cudaSuccess) return e;

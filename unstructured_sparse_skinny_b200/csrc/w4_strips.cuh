@@ -108,8 +108,9 @@ struct StripAt {
 
 // The whole product of this warp's strips, its share of K.  `row(n)` is the
 // n-th activation row, first asked for behind a barrier of the CTA; columns
-// behind K are not read, and count as zeros.
-template <typename T, int NG, int NT, typename Row>
+// behind K are not read, and count as zeros.  With two parts the rows from
+// `rows` on are the first ones' second parts.
+template <typename T, int NG, int NT, int Parts, typename Row>
 __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t units, int32_t K, int32_t rows,
                                               int pairs, uint8_t* smem, uint32_t smem_bytes, const Row& row,
                                               float (&acc)[2][NT][4]) {
@@ -127,18 +128,19 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
     if (begin + d * ways < units) load(buf[d], begin + d * ways);
   // A row's pitch leaves the rows 64 bytes apart modulo 128, so the eight lanes
   // of a shared-memory phase (two rows of 64 bytes) meet all banks once.
-  const int32_t chunk = min(units, (static_cast<int32_t>(smem_bytes) / rows - 64) / 256);
+  const int32_t chunk = min(units, (static_cast<int32_t>(smem_bytes) / (rows * Parts) - 64) / 256);
   const uint32_t row_pitch = chunk * 256 + 64;
   const int tiles = (rows + 7) / 8;
   uint32_t x[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) x[nt] = smem_u32(smem) + min(8 * nt + g, rows - 1) * row_pitch + 16 * t;
+  const uint32_t below = rows * row_pitch;  // from a row to its second part
   int32_t u = begin;
   int next = 0;  // place in buf of unit u
   for (int32_t from = 0; from < units; from += chunk) {
     const int32_t pieces = min(chunk, units - from) * 16;
     __syncthreads();  // what was in shared memory has been read
-    for (int32_t i = threadIdx.x; i < rows * pieces; i += kStripThreads) {
+    for (int32_t i = threadIdx.x; i < rows * Parts * pieces; i += kStripThreads) {
       const int32_t n = i / pieces, c = i - n * pieces;
       *reinterpret_cast<uint4*>(smem + n * row_pitch + c * 16) = load_act8<true>(row(n), from * kW4UnitCols + c * 8, K);
     }
@@ -149,19 +151,19 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
       for (int d = 0; d < kAhead; ++d) {
         if (d == next && u < end) {
           const uint32_t offset = (u - from) * 256;
-          const auto act = [&](int nt, int b, int) {
+          const auto act = [&](int nt, int b, int part) {
             uint4 v;
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(x[nt] + offset + b * 64)
+                         : "r"(x[nt] + offset + part * below + b * 64)
                          : "memory");
             return v;
           };
           // (a branch for a single tile: predicates alone leave the products of the others in the pipe)
           if (NT > 1 && tiles == 1)
-            strip_unit<T, NG, 2, 1, NT>(buf[d], 1, act, acc);
+            strip_unit<T, NG, 2, 1, NT, Parts>(buf[d], 1, act, acc);
           else
-            strip_unit<T, NG, 2, NT, NT>(buf[d], tiles, act, acc);
+            strip_unit<T, NG, 2, NT, NT, Parts>(buf[d], tiles, act, acc);
           if (u + kAhead * ways < units) load(buf[d], u + kAhead * ways);
           u += ways;
           next = next + 1 == kAhead ? 0 : next + 1;

@@ -106,6 +106,11 @@ struct StripAt {
       : record(A.at(unit)), pitch(8 * A.record), zeros(A.zeros) {}
 };
 
+// Copies 16 bytes to shared memory without waiting for them, or zeros.
+__device__ __forceinline__ void copy_or_zero(uint32_t to, const void* from, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(copy ? 16 : 0) : "memory");
+}
+
 // The whole product of this warp's strips, its share of K.  `row(n)` is the
 // n-th activation row, first asked for behind a barrier of the CTA; columns
 // behind K are not read, and count as zeros.  With two parts the rows from
@@ -141,9 +146,10 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
     const int32_t pieces = min(chunk, units - from) * 16;
     __syncthreads();  // what was in shared memory has been read
     for (int32_t i = threadIdx.x; i < rows * Parts * pieces; i += kStripThreads) {
-      const int32_t n = i / pieces, c = i - n * pieces;
-      *reinterpret_cast<uint4*>(smem + n * row_pitch + c * 16) = load_act8<true>(row(n), from * kW4UnitCols + c * 8, K);
+      const int32_t n = i / pieces, c = i - n * pieces, k = from * kW4UnitCols + c * 8;
+      copy_or_zero(smem_u32(smem) + n * row_pitch + c * 16, row(n) + (k < K ? k : 0), k < K);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     const int32_t end = min(units, from + chunk);
     while (u < end) {

@@ -454,6 +454,8 @@ struct ExpertParams {
 template <typename T, int NG, int NT, bool Gated>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  constexpr uint32_t rings = kStripWarps * StripRing<NG>::kBytes;
+  uint8_t* staged = smem + rings;
   __shared__ int32_t token[kMoeMaxTokens];
   griddep_wait();
   griddep_launch_dependents();
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
     const int32_t rows = min(slot.count - n0, NT * 8);
     float acc[2][NT][4] = {};
     strip_product<T, NG, NT, 1>(
-        at, A.units, p.H, rows, p.pairs, smem, p.shared, [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
+        at, A.units, p.H, rows, p.pairs, smem, staged, p.shared - rings, [&](int32_t n) { return p.X + token[n0 + n] * p.ldx; }, acc);
     const auto store = [&](int32_t n, int32_t f, float v) {
       // columns behind F pad h to 16 bytes: finite whatever x holds
       if (f >= p.ws.ldh) return;
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
       *h = rounded;
       h[p.rest] = from_float<T>(isfinite(left) ? left : 0.0f);  // of an h that rounds to infinity: nothing
     };
-    strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
+    strip_reduce<NT>(acc, p.pairs, rows, staged, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t f = (pair0 + i) * (Gated ? 16 : 32) + row;
       a = activate(p.activation, a);
       store(n, f, Gated ? a * b : a);
@@ -493,6 +495,8 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
 template <typename T, int NG, int NT>
 __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  constexpr uint32_t rings = kStripWarps * StripRing<NG>::kBytes;
+  uint8_t* staged = smem + rings;
   griddep_wait();
   griddep_launch_dependents();
   if (static_cast<int32_t>(blockIdx.y) >= *p.ws.running) return;
@@ -505,10 +509,10 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kerne
     const int32_t rows = min(slot.count - n0, NT * 8), first = slot.first + n0;
     float acc[2][NT][4] = {};
     strip_product<T, NG, NT, 2>(
-        at, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, p.shared,
+        at, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, staged, p.shared - rings,
         [&](int32_t n) { return p.ws.h + (n < rows ? first + n : first + n - rows) * p.ws.ldh + (n < rows ? 0 : p.rest); },
         acc);
-    strip_reduce<NT>(acc, p.pairs, rows, smem, [&](int i, int32_t n, int32_t row, float a, float b) {
+    strip_reduce<NT>(acc, p.pairs, rows, staged, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t m = (pair0 + i) * 32 + row;
       const float w = p.ws.pair_weight[first + n];
       float* y = p.ws.y + static_cast<int64_t>(first + n) * A.M;
@@ -679,7 +683,7 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
   const double share = c.top_k < E ? c.top_k / E : 1.0, running = E * (1.0 - std::pow(1.0 - share, c.tokens));
   int32_t all = gated ? p.gate.strips : (p.gate.strips + 1) / 2;
   p.pairs = pairs_per_cta(running, all, p.gate.units, pairs / running);
-  p.shared = strip_shared(rows, p.gate.units, NT);
+  p.shared = strip_shared<NG>(rows, p.gate.units, NT);
   e = launch_after(gate_up, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
                    1, s, p);
   if (e != cudaSuccess) return e;
@@ -688,7 +692,7 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
                         static_cast<T*>(c.out), c.ldo);
   all = (p.down.strips + 1) / 2;
   p.pairs = pairs_per_cta(running, all, p.down.units, 2 * pairs / running);
-  p.shared = strip_shared(2 * rows, p.down.units, NT);
+  p.shared = strip_shared<NG>(2 * rows, p.down.units, NT);
   e = launch_after(down, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared, 1,
                    s, p);
   if (e != cudaSuccess) return e;

@@ -26,16 +26,18 @@ namespace flashspmm {
 
 constexpr int kStripWarps = 8;
 constexpr int kStripThreads = kStripWarps * 32;
-constexpr int kStripShared = 108 * 1024;  // two CTAs on an SM
+constexpr int kStripShared = 112 * 1024;  // two CTAs on an SM
+constexpr int kStripRing = 4;             // units of a warp on their way to shared memory
 
 // One unit of a strip in a lane's registers.
 template <typename T, int NG>
 struct StripUnit {
   uint4 c[2];
   W4Groups<T, NG> g;
+  // `record` is in shared memory
   __device__ __forceinline__ void load(const uint8_t* record, int lane, bool zeros) {
-    c[0] = ld_stream(record + lane * 16);
-    c[1] = ld_stream(record + 512 + lane * 16);
+    c[0] = *reinterpret_cast<const uint4*>(record + lane * 16);
+    c[1] = *reinterpret_cast<const uint4*>(record + 512 + lane * 16);
     g.load(record, lane >> 2, zeros);
   }
   __device__ __forceinline__ uint32_t word(int i) const {
@@ -110,71 +112,104 @@ struct StripAt {
 __device__ __forceinline__ void copy_or_zero(uint32_t to, const void* from, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(copy ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// The shared memory a warp's units arrive in: places of a pair of records.
+template <int NG>
+struct StripRing {
+  static constexpr uint32_t kRecord = kW4CodeBytes + 48 * NG, kPlace = 2 * kRecord, kBytes = kStripRing * kPlace;
+  uint8_t* base;  // this warp's
+  // Starts the copies of one pair of records, one group of copies for wait().
+  __device__ __forceinline__ void ask(int place, const uint8_t* const (&from)[2], const StripAt (&at)[2], int lane) const {
+    const uint32_t to = smem_u32(base) + place * kPlace;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      copy16(to + r * kRecord + lane * 16, from[r] + lane * 16);
+      copy16(to + r * kRecord + 512 + lane * 16, from[r] + 512 + lane * 16);
+    }
+    // scales and zero points: half a warp a record
+    const int piece = lane & 15;
+    const bool second = lane >= 16;
+    if (piece < ((second ? at[1].zeros : at[0].zeros) ? 3 * NG : 2 * NG))
+      copy16(to + (second ? kRecord : 0) + kW4CodeBytes + piece * 16,
+             (second ? from[1] : from[0]) + kW4CodeBytes + piece * 16);
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The oldest of kStripRing groups has arrived, for the whole warp.
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStripRing - 1) : "memory");
+    __syncwarp();
+  }
+};
 
 // The whole product of this warp's strips, its share of K.  `row(n)` is the
 // n-th activation row, first asked for behind a barrier of the CTA; columns
 // behind K are not read, and count as zeros.  With two parts the rows from
-// `rows` on are the first ones' second parts.
+// `rows` on are the first ones' second parts.  `staged` is shared memory for
+// activations, behind the rings.
 template <typename T, int NG, int NT, int Parts, typename Row>
 __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t units, int32_t K, int32_t rows,
-                                              int pairs, uint8_t* smem, uint32_t smem_bytes, const Row& row,
-                                              float (&acc)[2][NT][4]) {
-  constexpr int kAhead = 2;
+                                              int pairs, uint8_t* rings, uint8_t* staged, uint32_t staged_bytes,
+                                              const Row& row, float (&acc)[2][NT][4]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int ways = kStripWarps / pairs;
-  StripUnit<T, NG> buf[kAhead][2];
-  const int32_t begin = warp / pairs;
-  const auto load = [&](StripUnit<T, NG> (&to)[2], int32_t u) {
+  const StripRing<NG> ring{rings + warp * StripRing<NG>::kBytes};
+  int32_t u = warp / pairs, asked = u;
+  const uint8_t* from[2] = {at[0].record + static_cast<int64_t>(u) * at[0].pitch,
+                            at[1].record + static_cast<int64_t>(u) * at[1].pitch};
+  const auto ask = [&](int place) {
+    if (asked < units) ring.ask(place, from, at, lane);
+    ring.commit();
+    asked += ways;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) to[r].load(at[r].record + static_cast<int64_t>(u) * at[r].pitch, lane, at[r].zeros);
+    for (int r = 0; r < 2; ++r) from[r] += static_cast<int64_t>(ways) * at[r].pitch;
   };
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d)
-    if (begin + d * ways < units) load(buf[d], begin + d * ways);
+  for (int d = 0; d < kStripRing; ++d) ask(d);
   // A row's pitch leaves the rows 64 bytes apart modulo 128, so the eight lanes
   // of a shared-memory phase (two rows of 64 bytes) meet all banks once.
-  const int32_t chunk = min(units, (static_cast<int32_t>(smem_bytes) / (rows * Parts) - 64) / 256);
+  const int32_t chunk = min(units, (static_cast<int32_t>(staged_bytes) / (rows * Parts) - 64) / 256);
   const uint32_t row_pitch = chunk * 256 + 64;
   const int tiles = (rows + 7) / 8;
   uint32_t x[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) x[nt] = smem_u32(smem) + min(8 * nt + g, rows - 1) * row_pitch + 16 * t;
+  for (int nt = 0; nt < NT; ++nt) x[nt] = smem_u32(staged) + min(8 * nt + g, rows - 1) * row_pitch + 16 * t;
   const uint32_t below = rows * row_pitch;  // from a row to its second part
-  int32_t u = begin;
-  int next = 0;  // place in buf of unit u
-  for (int32_t from = 0; from < units; from += chunk) {
-    const int32_t pieces = min(chunk, units - from) * 16;
+  int place = 0;                            // of unit u
+  for (int32_t first = 0; first < units; first += chunk) {
+    const int32_t pieces = min(chunk, units - first) * 16;
     __syncthreads();  // what was in shared memory has been read
     for (int32_t i = threadIdx.x; i < rows * Parts * pieces; i += kStripThreads) {
-      const int32_t n = i / pieces, c = i - n * pieces, k = from * kW4UnitCols + c * 8;
-      copy_or_zero(smem_u32(smem) + n * row_pitch + c * 16, row(n) + (k < K ? k : 0), k < K);
+      const int32_t n = i / pieces, c = i - n * pieces, k = first * kW4UnitCols + c * 8;
+      copy_or_zero(smem_u32(staged) + n * row_pitch + c * 16, row(n) + (k < K ? k : 0), k < K);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    const int32_t end = min(units, from + chunk);
-    while (u < end) {
+    for (const int32_t end = min(units, first + chunk); u < end; u += ways) {
+      const uint32_t offset = (u - first) * 256;
+      const auto act = [&](int nt, int b, int part) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(x[nt] + offset + part * below + b * 64)
+                     : "memory");
+        return v;
+      };
+      ring.wait();
+      StripUnit<T, NG> unit[2];
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        if (d == next && u < end) {
-          const uint32_t offset = (u - from) * 256;
-          const auto act = [&](int nt, int b, int part) {
-            uint4 v;
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(x[nt] + offset + part * below + b * 64)
-                         : "memory");
-            return v;
-          };
-          // (a branch for a single tile: predicates alone leave the products of the others in the pipe)
-          if (NT > 1 && tiles == 1)
-            strip_unit<T, NG, 2, 1, NT, Parts>(buf[d], 1, act, acc);
-          else
-            strip_unit<T, NG, 2, NT, NT, Parts>(buf[d], tiles, act, acc);
-          if (u + kAhead * ways < units) load(buf[d], u + kAhead * ways);
-          u += ways;
-          next = next + 1 == kAhead ? 0 : next + 1;
-        }
-      }
+      for (int r = 0; r < 2; ++r)
+        unit[r].load(ring.base + place * ring.kPlace + r * ring.kRecord, lane, at[r].zeros);
+      // (a branch for a single tile: predicates alone leave the products of the others in the pipe)
+      if (NT > 1 && tiles == 1)
+        strip_unit<T, NG, 2, 1, NT, Parts>(unit, 1, act, acc);
+      else
+        strip_unit<T, NG, 2, NT, NT, Parts>(unit, tiles, act, acc);
+      __syncwarp();
+      ask(place);
+      place = place + 1 == kStripRing ? 0 : place + 1;
     }
   }
 }
@@ -227,12 +262,14 @@ inline int32_t pairs_per_cta(double sets, int32_t pairs, int32_t units, double r
   return best;
 }
 
-// Host: dynamic shared memory for up to `rows` activation rows of `units`
-// units and for the sums of tiles of NT.
+// Host: dynamic shared memory for the rings, up to `rows` activation rows of
+// `units` units and the sums of tiles of NT.
+template <int NG>
 inline uint32_t strip_shared(int32_t rows, int32_t units, int NT) {
+  constexpr int64_t rings = kStripWarps * StripRing<NG>::kBytes;
   const int64_t sums = static_cast<int64_t>(kStripWarps) * NT * 8 * 36 * 4;
   const int64_t staged = static_cast<int64_t>(rows) * (static_cast<int64_t>(units) * 256 + 64);
-  return static_cast<uint32_t>(max64(sums, min64(staged, kStripShared)));
+  return static_cast<uint32_t>(rings + max64(sums, min64(staged, kStripShared - rings)));
 }
 
 }  // namespace flashspmm

@@ -532,7 +532,7 @@ constexpr int kDirectWarps = 16, kDirectSlots = kDirectTokens * kMoeMaxTopK;
 template <typename T, int NG>
 __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(const ExpertParams p,
                                                                                T* __restrict__ out, int64_t ldo) {
-  constexpr int kAhead = 2;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Slot slots[kDirectSlots];
   __shared__ float weight[kDirectSlots][kDirectTokens];
   __shared__ float red[kDirectWarps][kDirectTokens][36];  // 32 rows, and the fragments' stores meet all banks
@@ -553,56 +553,88 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
   const int32_t from = static_cast<int32_t>(items * warp / kDirectWarps);
   const int32_t to = static_cast<int32_t>(items * (warp + 1) / kDirectWarps);
   const W4Dev& A = p.down;
-  int32_t s_load = from / units, u_load = from - s_load * units;  // of the next record to be read
-  const auto load = [&](StripUnit<T, NG> (&unit)[2]) {
+  const StripRing<NG> ring{smem + warp * StripRing<NG>::kBytes};
+  const int32_t s0 = from / units, u0 = from - s0 * units;
+  // the next records to be asked for
+  int32_t asked = from, s_ask = s0, u_ask = u0;
+  const StripAt at[2] = {StripAt(A, 0), StripAt(A, 0)};
+  const uint8_t* record[2];
+  const auto seek = [&](int32_t unit) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) unit[r].load(A.at(A.unit(slots[s_load].expert, strip[r], u_load)), lane, A.zeros);
-    if (++u_load == units) {
-      u_load = 0;
-      ++s_load;
-    }
+    for (int r = 0; r < 2; ++r) record[r] = A.at(A.unit(slots[s_ask].expert, strip[r], unit));
   };
-  StripUnit<T, NG> buf[kAhead][2];
+  const auto ask = [&](int place) {
+    if (asked < to) {
+      ring.ask(place, record, at, lane);
+      ++asked;
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d)
-    if (from + d < to) load(buf[d]);
-  int32_t s = from / units, u = from - s * units;
-  float total[2][4] = {}, acc[2][1][4] = {};
+      for (int r = 0; r < 2; ++r) record[r] += at[r].pitch;
+      if (++u_ask == units) {
+        u_ask = 0;
+        ++s_ask;
+        if (asked < to) seek(0);
+      }
+    }
+    ring.commit();
+  };
+  if (from < to) seek(u0);
+#pragma unroll
+  for (int d = 0; d < kStripRing; ++d) ask(d);
+  // the next activations: a lane's registers of a block are filled for the next unit as soon as they are free
+  int32_t s_x = s0, u_x = u0;
   const uint16_t* row = nullptr;
-  bool fresh = true;
-  for (int32_t base = from; base < to; base += kAhead) {
+  const auto seek_row = [&] {
+    const uint32_t tokens = slots[s_x].tokens;
+    row = tokens >> g & 1 ? p.ws.h + (slots[s_x].first + __popc(tokens & ((1u << g) - 1))) * p.ws.ldh + 8 * t : nullptr;
+  };
+  uint4 x[4][2];
+  const auto load_x = [&](int b, int part) {
+    x[b][part] = make_uint4(0, 0, 0, 0);
+    if (row && u_x * kW4UnitCols + 32 * b + 8 * t < p.ws.ldh)
+      x[b][part] = *reinterpret_cast<const uint4*>(row + (part ? p.rest : 0) + u_x * kW4UnitCols + 32 * b);
+  };
+  if (from < to) {
+    seek_row();
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      const int32_t i = base + d;
-      if (i >= to) break;
-      if (fresh) {
-        const uint32_t tokens = slots[s].tokens;
-        row = tokens >> g & 1 ? p.ws.h + (slots[s].first + __popc(tokens & ((1u << g) - 1))) * p.ws.ldh + 8 * t : nullptr;
-        fresh = false;
-      }
-      uint4 x[4][2];
+    for (int b = 0; b < 4; ++b) {
+      load_x(b, 0);
+      load_x(b, 1);
+    }
+  }
+  int32_t s = s0, u = u0;
+  float total[2][4] = {}, acc[2][1][4] = {};
+  int place = 0;
+  for (int32_t i = from; i < to; ++i) {
+    if (++u_x == units) {
+      u_x = 0;
+      ++s_x;
+      if (i + 1 < to) seek_row();
+    }
+    if (i + 1 == to) row = nullptr;
+    ring.wait();
+    StripUnit<T, NG> unit[2];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        x[b][0] = x[b][1] = make_uint4(0, 0, 0, 0);
-        if (row && u * kW4UnitCols + 32 * b + 8 * t < p.ws.ldh) {
-          x[b][0] = *reinterpret_cast<const uint4*>(row + u * kW4UnitCols + 32 * b);
-          x[b][1] = *reinterpret_cast<const uint4*>(row + p.rest + u * kW4UnitCols + 32 * b);
+    for (int r = 0; r < 2; ++r) unit[r].load(ring.base + place * ring.kPlace + r * ring.kRecord, lane, A.zeros);
+    strip_unit<T, NG, 2, 1, 1, 2>(unit, 1,
+                                  [&](int, int b, int part) {
+                                    const uint4 v = x[b][part];
+                                    load_x(b, part);
+                                    return v;
+                                  },
+                                  acc);
+    __syncwarp();
+    ask(place);
+    place = place + 1 == kStripRing ? 0 : place + 1;
+    if (++u == units || i + 1 == to) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          total[r][k] = fmaf(weight[s][2 * t + (k & 1)], acc[r][0][k], total[r][k]);
+          acc[r][0][k] = 0.0f;
         }
-      }
-      strip_unit<T, NG, 2, 1, 1, 2>(buf[d], 1, [&](int, int b, int part) { return x[b][part]; }, acc);
-      if (i + kAhead < to) load(buf[d]);
-      if (++u == units || i + 1 == to) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            total[r][k] = fmaf(weight[s][2 * t + (k & 1)], acc[r][0][k], total[r][k]);
-            acc[r][0][k] = 0.0f;
-          }
-        u = 0;
-        ++s;
-        fresh = true;
-      }
+      u = 0;
+      ++s;
     }
   }
 #pragma unroll
@@ -666,6 +698,7 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
   const bool gated = c.up.data != nullptr;
   auto gate_up = gated ? moe_gate_up_kernel<T, NG, NT, true> : moe_gate_up_kernel<T, NG, NT, false>;
   auto down = moe_down_kernel<T, NG, NT>;
+  auto direct = moe_down_direct_kernel<T, NG>;
   static std::atomic<uint64_t> allowed[2];  // devices on which the kernels may use their shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -673,6 +706,9 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
   if (!(allowed[gated].load() >> (dev & 63) & 1)) {
     e = cudaFuncSetAttribute(gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kDirectWarps * StripRing<NG>::kBytes);
     if (e != cudaSuccess) return e;
     allowed[gated].fetch_or(uint64_t(1) << (dev & 63));
   }
@@ -688,7 +724,7 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
                    1, s, p);
   if (e != cudaSuccess) return e;
   if (c.tokens <= kDirectTokens)
-    return launch_after(moe_down_direct_kernel<T, NG>, dim3((p.down.strips + 1) / 2), kDirectWarps * 32, 0, 1, s, p,
+    return launch_after(direct, dim3((p.down.strips + 1) / 2), kDirectWarps * 32, kDirectWarps * StripRing<NG>::kBytes, 1, s, p,
                         static_cast<T*>(c.out), c.ldo);
   all = (p.down.strips + 1) / 2;
   p.pairs = pairs_per_cta(running, all, p.down.units, 2 * pairs / running);

@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
   const int32_t s0 = from / units, u0 = from - s0 * units;
   // the next records to be asked for
   int32_t asked = from, s_ask = s0, u_ask = u0;
-  const StripAt at[2] = {StripAt(A, 0), StripAt(A, 0)};
+  const bool zeros[2] = {A.zeros, A.zeros};
   const uint8_t* record[2];
   const auto seek = [&](int32_t unit) {
 #pragma unroll
@@ -565,10 +565,10 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
   };
   const auto ask = [&](int place) {
     if (asked < to) {
-      ring.ask(place, record, at, lane);
+      ring.ask(place, record, zeros, lane);
       ++asked;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) record[r] += at[r].pitch;
+      for (int r = 0; r < 2; ++r) record[r] += 8 * A.record;
       if (++u_ask == units) {
         u_ask = 0;
         ++s_ask;
@@ -724,8 +724,8 @@ cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
                    1, s, p);
   if (e != cudaSuccess) return e;
   if (c.tokens <= kDirectTokens)
-    return launch_after(direct, dim3((p.down.strips + 1) / 2), kDirectWarps * 32, kDirectWarps * StripRing<NG>::kBytes, 1, s, p,
-                        static_cast<T*>(c.out), c.ldo);
+    return launch_after(direct, dim3((p.down.strips + 1) / 2), kDirectWarps * 32,
+                        kDirectWarps * StripRing<NG>::kBytes, 1, s, p, static_cast<T*>(c.out), c.ldo);
   all = (p.down.strips + 1) / 2;
   p.pairs = pairs_per_cta(running, all, p.down.units, 2 * pairs / running);
   p.shared = strip_shared<NG>(2 * rows, p.down.units, NT);

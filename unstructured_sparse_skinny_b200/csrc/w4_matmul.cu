@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
   StripUnit<T, NG> buf[kAhead][1];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
-    if (warp + d * kMatmulWarps < units) buf[d][0].load(strip + static_cast<int64_t>(warp + d * kMatmulWarps) * pitch, lane, p.A.zeros);
+    if (warp + d * kMatmulWarps < units) buf[d][0].read(strip + static_cast<int64_t>(warp + d * kMatmulWarps) * pitch, lane, p.A.zeros);
   float acc[1][1][4] = {};
   for (int32_t base = warp; base < units; base += kAhead * kMatmulWarps) {
 #pragma unroll
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
       }
       strip_unit<T, NG, 1, 1, 1>(buf[d], 1, [&](int, int b, int) { return x[b]; }, acc);
       const int32_t next = u + kAhead * kMatmulWarps;
-      if (next < units) buf[d][0].load(strip + static_cast<int64_t>(next) * pitch, lane, p.A.zeros);
+      if (next < units) buf[d][0].read(strip + static_cast<int64_t>(next) * pitch, lane, p.A.zeros);
     }
   }
 #pragma unroll

@@ -34,7 +34,13 @@ template <typename T, int NG>
 struct StripUnit {
   uint4 c[2];
   W4Groups<T, NG> g;
-  // `record` is in shared memory
+  // from global memory
+  __device__ __forceinline__ void read(const uint8_t* record, int lane, bool zeros) {
+    c[0] = ld_stream(record + lane * 16);
+    c[1] = ld_stream(record + 512 + lane * 16);
+    g.load(record, lane >> 2, zeros);
+  }
+  // from shared memory
   __device__ __forceinline__ void load(const uint8_t* record, int lane, bool zeros) {
     c[0] = *reinterpret_cast<const uint4*>(record + lane * 16);
     c[1] = *reinterpret_cast<const uint4*>(record + 512 + lane * 16);
@@ -122,7 +128,7 @@ struct StripRing {
   static constexpr uint32_t kRecord = kW4CodeBytes + 48 * NG, kPlace = 2 * kRecord, kBytes = kStripRing * kPlace;
   uint8_t* base;  // this warp's
   // Starts the copies of one pair of records, one group of copies for wait().
-  __device__ __forceinline__ void ask(int place, const uint8_t* const (&from)[2], const StripAt (&at)[2], int lane) const {
+  __device__ __forceinline__ void ask(int place, const uint8_t* const (&from)[2], const bool (&zeros)[2], int lane) const {
     const uint32_t to = smem_u32(base) + place * kPlace;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -132,7 +138,7 @@ struct StripRing {
     // scales and zero points: half a warp a record
     const int piece = lane & 15;
     const bool second = lane >= 16;
-    if (piece < ((second ? at[1].zeros : at[0].zeros) ? 3 * NG : 2 * NG))
+    if (piece < ((second ? zeros[1] : zeros[0]) ? 3 * NG : 2 * NG))
       copy16(to + (second ? kRecord : 0) + kW4CodeBytes + piece * 16,
              (second ? from[1] : from[0]) + kW4CodeBytes + piece * 16);
   }
@@ -159,8 +165,9 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
   int32_t u = warp / pairs, asked = u;
   const uint8_t* from[2] = {at[0].record + static_cast<int64_t>(u) * at[0].pitch,
                             at[1].record + static_cast<int64_t>(u) * at[1].pitch};
+  const bool zeros[2] = {at[0].zeros, at[1].zeros};
   const auto ask = [&](int place) {
-    if (asked < units) ring.ask(place, from, at, lane);
+    if (asked < units) ring.ask(place, from, zeros, lane);
     ring.commit();
     asked += ways;
 #pragma unroll

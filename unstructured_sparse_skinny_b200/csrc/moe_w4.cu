@@ -452,7 +452,7 @@ struct ExpertParams {
 // (Without that an output has 1.5 times the error that its own rounding makes: a
 // few large h carry it.  The second products cost a tenth of the layer.)
 template <typename T, int NG, int NT, bool Gated>
-__global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_kernel(const ExpertParams p) {
+__global__ void __launch_bounds__(kStripThreads, strip_ctas(NT)) moe_gate_up_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr uint32_t rings = kStripWarps * StripRing<NG>::kBytes;
   uint8_t* staged = smem + rings;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_gate_up_ke
 
 // y[pair] = weight * down h for some pairs of strips of a running expert.
 template <typename T, int NG, int NT>
-__global__ void __launch_bounds__(kStripThreads, NT == 4 ? 1 : 2) moe_down_kernel(const ExpertParams p) {
+__global__ void __launch_bounds__(kStripThreads, strip_ctas(NT)) moe_down_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr uint32_t rings = kStripWarps * StripRing<NG>::kBytes;
   uint8_t* staged = smem + rings;
@@ -693,48 +693,54 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
-template <typename T, int NG, int NT>
-cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
-  const bool gated = c.up.data != nullptr;
-  auto gate_up = gated ? moe_gate_up_kernel<T, NG, NT, true> : moe_gate_up_kernel<T, NG, NT, false>;
-  auto down = moe_down_kernel<T, NG, NT>;
-  auto direct = moe_down_direct_kernel<T, NG>;
-  static std::atomic<uint64_t> allowed[2];  // devices on which the kernels may use their shared memory
+// Once per device: the kernel may use this much shared memory.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, std::atomic<uint64_t>& allowed, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (!(allowed[gated].load() >> (dev & 63) & 1)) {
-    e = cudaFuncSetAttribute(gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripShared);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kDirectWarps * StripRing<NG>::kBytes);
-    if (e != cudaSuccess) return e;
-    allowed[gated].fetch_or(uint64_t(1) << (dev & 63));
-  }
+  if (e != cudaSuccess || (allowed.load() >> (dev & 63) & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) allowed.fetch_or(uint64_t(1) << (dev & 63));
+  return e;
+}
+
+template <typename T, int NG, int NT, bool Gated>
+cudaError_t experts_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed[2];
   const int64_t most = min64(c.gate.count, static_cast<int64_t>(c.tokens) * c.top_k);
   const int32_t rows = c.tokens < NT * 8 ? c.tokens : NT * 8;
   // experts that run and their tokens, as even routing has them
   const double E = c.gate.count, pairs = static_cast<double>(c.tokens) * c.top_k;
   const double share = c.top_k < E ? c.top_k / E : 1.0, running = E * (1.0 - std::pow(1.0 - share, c.tokens));
-  int32_t all = gated ? p.gate.strips : (p.gate.strips + 1) / 2;
-  p.pairs = pairs_per_cta(running, all, p.gate.units, pairs / running);
+  auto gate_up = moe_gate_up_kernel<T, NG, NT, Gated>;
+  cudaError_t e = allow_shared(gate_up, allowed[0], strip_limit(NT));
+  if (e != cudaSuccess) return e;
+  int32_t all = Gated ? p.gate.strips : (p.gate.strips + 1) / 2;
+  p.pairs = pairs_per_cta(running, all, p.gate.units, pairs / running, strip_ctas(NT));
   p.shared = strip_shared<NG>(rows, p.gate.units, NT);
   e = launch_after(gate_up, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
                    1, s, p);
   if (e != cudaSuccess) return e;
-  if (c.tokens <= kDirectTokens)
-    return launch_after(direct, dim3((p.down.strips + 1) / 2), kDirectWarps * 32,
-                        kDirectWarps * StripRing<NG>::kBytes, 1, s, p, static_cast<T*>(c.out), c.ldo);
   all = (p.down.strips + 1) / 2;
-  p.pairs = pairs_per_cta(running, all, p.down.units, 2 * pairs / running);
-  p.shared = strip_shared<NG>(2 * rows, p.down.units, NT);
-  e = launch_after(down, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared, 1,
-                   s, p);
-  if (e != cudaSuccess) return e;
-  return launch_after(moe_join_kernel<T>, dim3((p.down.M + 255) / 256, c.tokens), 256, 0, 1, s,
-                      static_cast<const float*>(p.ws.y), static_cast<const int32_t*>(p.ws.place), c.top_k, p.down.M,
-                      static_cast<T*>(c.out), c.ldo);
+  if constexpr (NT == 1) {  // up to kDirectTokens tokens
+    constexpr uint32_t rings = kDirectWarps * StripRing<NG>::kBytes;
+    auto down = moe_down_direct_kernel<T, NG>;
+    e = allow_shared(down, allowed[1], rings);
+    if (e != cudaSuccess) return e;
+    return launch_after(down, dim3(all), kDirectWarps * 32, rings, 1, s, p, static_cast<T*>(c.out), c.ldo);
+  } else {
+    auto down = moe_down_kernel<T, NG, NT>;
+    e = allow_shared(down, allowed[1], strip_limit(NT));
+    if (e != cudaSuccess) return e;
+    p.pairs = pairs_per_cta(running, all, p.down.units, 2 * pairs / running, strip_ctas(NT));
+    p.shared = strip_shared<NG>(2 * rows, p.down.units, NT);
+    e = launch_after(down, dim3((all + p.pairs - 1) / p.pairs, static_cast<unsigned>(most)), kStripThreads, p.shared,
+                     1, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_after(moe_join_kernel<T>, dim3((p.down.M + 255) / 256, c.tokens), 256, 0, 1, s,
+                        static_cast<const float*>(p.ws.y), static_cast<const int32_t*>(p.ws.place), c.top_k, p.down.M,
+                        static_cast<T*>(c.out), c.ldo);
+  }
 }
 
 template <typename T, typename RT>
@@ -781,14 +787,17 @@ cudaError_t layer_as(const MoeCall& c, ExpertParams& p, cudaStream_t s) {
   // Tokens that an expert's codes serve at a time: 8, 16 or 32.  An expert with more reads its codes again; 32
   // leave an SM half as many warps, and are for experts that get more than 12 on average.
   const bool many = static_cast<int64_t>(c.tokens) * c.top_k > 12 * static_cast<int64_t>(E);
-#define FLASHSPMM_EXPERTS(NG)                                  \
-  c.tokens <= 8             ? experts_as<T, NG, 1>(c, p, s)    \
-  : c.tokens <= 16 || !many ? experts_as<T, NG, 2>(c, p, s)    \
-                            : experts_as<T, NG, 4>(c, p, s)
+  const bool gated = c.up.data != nullptr;
+#define FLASHSPMM_EXPERTS_OF(NG, NT) (gated ? experts_as<T, NG, NT, true>(c, p, s) : experts_as<T, NG, NT, false>(c, p, s))
+#define FLASHSPMM_EXPERTS(NG)                                        \
+  c.tokens <= kDirectTokens ? FLASHSPMM_EXPERTS_OF(NG, 1)            \
+  : c.tokens <= 16 || !many ? FLASHSPMM_EXPERTS_OF(NG, 2)            \
+                            : FLASHSPMM_EXPERTS_OF(NG, 4)
   return c.gate.group == 128  ? FLASHSPMM_EXPERTS(1)
          : c.gate.group == 64 ? FLASHSPMM_EXPERTS(2)
                               : FLASHSPMM_EXPERTS(4);
 #undef FLASHSPMM_EXPERTS
+#undef FLASHSPMM_EXPERTS_OF
 }
 
 }  // namespace

@@ -1,17 +1,19 @@
 // The product of strips of 4-bit rows with a few activation rows, on the
 // tensor cores through mma.sync: the engine of the experts' products.
 //
-// Two CTAs of eight warps share an SM.  A warp has a pair of strips (two of one
+// CTAs of eight warps share an SM.  A warp has a pair of strips (two of one
 // matrix, or the same of two matrices), whose fragments use each 16 bytes of
 // activations twice; a CTA takes `pairs` pairs (1, 2, 4 or 8) and splits K among
-// the warps of a pair.  A warp reads its records straight to registers, two
-// units ahead; each lane finds its own fragments there.  The activations are
-// staged in shared memory once and serve all strips of the CTA.  Warps meet only
-// where the activations do not fit at once, and at the end, to add up K.  What
-// bounds it is the rate at which the warps turn codes into fragments, some 160
-// instructions a record.  (Sixteen warps with one strip each, 64 registers, read
-// the activations from shared memory twice as often: 310 instead of 255 us for
-// both products of 64 tokens, 64 experts of 4096 x 2048.)
+// the warps of a pair.  A warp's records arrive by asynchronous copies in a ring
+// of its own in shared memory, two units ahead: no other warp waits for them,
+// and the registers they would fill are free for fragments (64 tokens, 64 experts
+// of 4096 x 2048: 271 us for the layer, with two units ahead in registers 312;
+// four units ahead leave less room for activations, 283).  The activations are
+// staged in shared memory, as many units as fit at a time, and serve all strips
+// of the CTA.  Warps meet only there, and at the end, to add up K.  What bounds
+// it is the rate at which the warps turn codes into fragments: 178 instructions
+// a record, issued in 63 % of the cycles, at half the rate of HBM.  (Sixteen
+// warps with one strip each read the activations twice as often: a fifth slower.)
 //
 // A group's weights enter the product as whole numbers q - z, and the fp32 sum
 // of the group is scaled: no weight is rounded.
@@ -26,8 +28,14 @@ namespace flashspmm {
 
 constexpr int kStripWarps = 8;
 constexpr int kStripThreads = kStripWarps * 32;
-constexpr int kStripShared = 112 * 1024;  // two CTAs on an SM
-constexpr int kStripRing = 4;             // units of a warp on their way to shared memory
+constexpr int kStripRing = 2;  // units of a warp on their way to shared memory
+
+// CTAs that an SM holds, by the tiles of eight activation rows of their warps,
+// and the shared memory of one.  (One tile: three in 80 registers a thread, 130
+// us instead of 134 for 4 tokens, 8 experts of 4096 x 11008.  Two tiles spill
+// there, 271 -> 356 us for 64 tokens, 64 experts of 4096 x 2048.)
+constexpr int strip_ctas(int NT) { return NT == 1 ? 3 : NT == 2 ? 2 : 1; }
+constexpr int strip_limit(int NT) { return (NT == 1 ? 74 : NT == 2 ? 112 : 224) * 1024; }
 
 // One unit of a strip in a lane's registers.
 template <typename T, int NG>
@@ -253,9 +261,9 @@ __device__ __forceinline__ void strip_reduce(const float (&acc)[2][NT][4], int p
 // is its records', the staging of the activations and a fixed part, in records
 // (22 KB/us for each of 296 CTAs at the rate of HBM: a record is 0.05 us, the
 // fixed part some 3 us; staging a row's unit is a tenth of a record).
-inline int32_t pairs_per_cta(double sets, int32_t pairs, int32_t units, double rows) {
+inline int32_t pairs_per_cta(double sets, int32_t pairs, int32_t units, double rows, int resident) {
   const int sms = device_sm_count();
-  const double wave = 2.0 * (sms > 0 ? sms : 1);
+  const double wave = static_cast<double>(resident) * (sms > 0 ? sms : 1);
   int32_t best = 1;
   double least = 0.0;
   for (int32_t take = 1; take <= kStripWarps; take *= 2) {
@@ -276,7 +284,7 @@ inline uint32_t strip_shared(int32_t rows, int32_t units, int NT) {
   constexpr int64_t rings = kStripWarps * StripRing<NG>::kBytes;
   const int64_t sums = static_cast<int64_t>(kStripWarps) * NT * 8 * 36 * 4;
   const int64_t staged = static_cast<int64_t>(rows) * (static_cast<int64_t>(units) * 256 + 64);
-  return static_cast<uint32_t>(rings + max64(sums, min64(staged, kStripShared - rings)));
+  return static_cast<uint32_t>(rings + max64(sums, min64(staged, strip_limit(NT) - rings)));
 }
 
 }  // namespace flashspmm

@@ -166,6 +166,12 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t nthreads,
   return r != 0;
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
 // Word `slot` of this lane in a load round, or the sentinel when the slot is
 // past the lane's `nvalid` words (the address is then not dereferenced).
 // Read-only path, no L1 allocation, evict-first in L2: every word is used

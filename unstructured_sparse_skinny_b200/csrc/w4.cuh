@@ -5,11 +5,10 @@
 // to a block of 128, and units of 128 columns.  A unit of one strip is one
 // record: 1024 bytes of codes, its scales and, if there are any, its zero
 // points.  The records of a block's eight strips follow one another, then come
-// the block's next 128 columns: a bulk copy costs the SM that issues it about
-// 100 ns whatever its size, so a block's unit, or some strips of it, is one
-// copy.  A warp reads a record's codes with two 16-byte loads per lane, and every lane then holds
-// exactly the codes of its own mma.m16n8k16 A fragments, so nothing is
-// shuffled or staged.  Lane l = 4 * g + t owns rows g and g + 8 and, in each
+// the block's next 128 columns, so a block's unit, or some strips of it, is one
+// bulk copy.  A warp reads a record's codes with two 16-byte loads per lane, and
+// every lane then holds exactly the codes of its own mma.m16n8k16 A fragments, so
+// nothing is shuffled.  Lane l = 4 * g + t owns rows g and g + 8 and, in each
 // 32-column block b of the unit, the eight columns 32 * b + 8 * t .. + 7.  The
 // order of K inside a product is free as long as both operands use the same
 // one: step s of block b takes columns 8 * t + 4 * s + {0, 1} as the

@@ -90,6 +90,21 @@ __global__ void __launch_bounds__(256) w4_stage_kernel(const uint16_t* __restric
 
 // ---------------------------------------------------------------- primitives
 
+// Untiled bulk load; both addresses 16-byte aligned, the size a multiple of 16.
+__device__ __forceinline__ void bulk_load(void* smem, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
 // 16 TMEM lanes x 32 columns: register 2 i is row g, 2 i + 1 row g + 8 of column 4 i + t.
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(

@@ -2,7 +2,7 @@
 
 Bound of one output, counted from the roundings: sums as in test_w4_gpu.py
 (d = (K / 16 + 64) * 2^-23 of the sum of magnitudes), the activation's slope of
-at most 1.13 and its own error of at most 2^-20, h rounded to 16 bits (eps / 2), the
+at most 1.13 and its own error of at most 2^-20, h rounded to 16 bits (eps / 2; it is kept better), the
 weights' error of at most 2^-20, and the output's rounding (eps / 2).
 """
 import pytest
@@ -96,6 +96,19 @@ def test_layer(T, E, k, H, F, dtype):
     check(out, *experts64(X, ids, weights, dense, act, dtype))
     again = fs.moe_w4_experts(X, ids, weights, *packed, activation=act)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("T,H,F,group,dtype", [(8, 6152, 2100, 32, torch.bfloat16), (8, 4096, 4104, 128, torch.float16),
+                                               (16, 4360, 2568, 64, torch.float16), (13, 2568, 6280, 32, torch.bfloat16),
+                                               (33, 5000, 1208, 128, torch.bfloat16)])
+def test_long_rows(T, H, F, group, dtype):
+    """Activations that shared memory holds in several parts, and a second pass over an expert's records."""
+    dense, packed = layer(2, H, F, group, dtype, seed=T)
+    X = torch.randn((T, H), device="cuda", generator=gen(T)).to(dtype)
+    ids = torch.tensor([0, 1], device="cuda", dtype=torch.int32).repeat(T, 1)
+    weights = torch.rand((T, 2), device="cuda", generator=gen(1))
+    out = fs.moe_w4_experts(X, ids, weights, *packed)
+    check(out, *experts64(X, ids, weights, dense, "silu", dtype))
 
 
 @pytest.mark.parametrize("up", [True, False])

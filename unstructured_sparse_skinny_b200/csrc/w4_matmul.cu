@@ -20,9 +20,13 @@ struct MatmulParams {
 
 // One strip of 16 rows and eight tokens a CTA: its warps have the units in
 // turn and add up at the end.  Codes come two units ahead; the activations,
-// which all CTAs read again, from L1 and L2 as the fragments need them.  (Staged
-// in shared memory first, they delay the short-lived CTAs more than they save:
-// 29 and 54 us for one and eight tokens of 12288^2.)
+// which all CTAs read again, from L1 and L2 as the fragments need them.  What
+// bounds it is turning codes into fragments, 156 instructions a record: one and
+// eight tokens of 12288^2 take 23 and 25 us, one of 49152 x 12288 71, two thirds
+// of what HBM allows.  (Activations staged in shared memory first delay the
+// short-lived CTAs more than they save, 29 and 54 us; CTAs that stay and read on
+// into the next strip, 84 for 49152 x 12288; codes through a ring in shared
+// memory, 78.)
 template <typename T, int NG>
 __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const MatmulParams p) {
   constexpr int kAhead = 2;

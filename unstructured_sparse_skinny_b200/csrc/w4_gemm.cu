@@ -19,8 +19,8 @@
 // them in their order.  Four warps do this behind the products; at the end of
 // its run the whole CTA joins in, since nothing is left to overlap with.
 //
-// What bounds it: up to 128 tokens the warps that make the weights, some 670
-// cycles a unit (12288^2, 64 tokens: 36 us; HBM would allow 12); at 256 tokens the
+// What bounds it: up to 128 tokens the warps that make the weights (12288^2, 64
+// tokens: 32 us; HBM would allow 12); at 256 tokens the
 // products, 1024 cycles a unit, and the clock under the power limit (9216 x 36864:
 // 135 to 148 us, 1.2 to 1.3 PFLOP/s).  Some 8 us a call are fixed: two kernels, the
 // ends of the runs and the joining of shared blocks.
@@ -120,6 +120,16 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[1
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 TMEM lanes x 64 columns, likewise.
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
+  uint32_t half[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) half[i] = r[16 * h + i];
+    tmem_store(taddr + 32 * h, half);
+  }
+}
 // 16 TMEM lanes x 16 columns, likewise.
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
@@ -161,12 +171,15 @@ struct Part {
   uint32_t s[kGroups], z[kGroups];                       // {row g, row g + 8}
 
   __device__ __forceinline__ void load(const uint8_t* record, int part, int lane, bool zeros) {
-    if (P == 2) {
-      const uint4 v = *reinterpret_cast<const uint4*>(record + part * 512 + lane * 16);
-      w[0] = v.x;
-      w[1] = v.y;
-      w[2 % kWords] = v.z;
-      w[3 % kWords] = v.w;
+    if (P == 1) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(record + i * 512 + lane * 16);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[(4 * i + 2) % kWords] = v.z;
+        w[(4 * i + 3) % kWords] = v.w;
+      }
     } else {
       const uint2 v = *reinterpret_cast<const uint2*>(record + (part >> 1) * 512 + lane * 16 + (part & 1) * 8);
       w[0] = v.x;
@@ -178,6 +191,17 @@ struct Part {
     if (kGroups == 1) {
       s[0] = *reinterpret_cast<const uint32_t*>(scales);
       z[0] = zeros ? *reinterpret_cast<const uint16_t*>(points) : 0x0808u;
+    } else if (kGroups == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(scales);
+      s[0] = v.x;
+      s[1 % kGroups] = v.y;
+      s[2 % kGroups] = v.z;
+      s[kGroups - 1] = v.w;
+      const uint2 q = zeros ? *reinterpret_cast<const uint2*>(points) : make_uint2(0x08080808u, 0x08080808u);
+      z[0] = q.x & 0xFFFF;
+      z[1 % kGroups] = q.x >> 16;
+      z[2 % kGroups] = q.y & 0xFFFF;
+      z[kGroups - 1] = q.y >> 16;
     } else {
       const uint2 v = *reinterpret_cast<const uint2*>(scales);
       s[0] = v.x;
@@ -371,7 +395,7 @@ __device__ __forceinline__ void join_block(const GemmParams& p, int32_t block, c
   }
 }
 
-// P: warps share the columns of 32 rows of a unit P ways, so 4 / P groups of 4 P warps have units in turn.
+// P (1 or 4): warps share the columns of 32 rows of a unit P ways, so 4 / P groups of 4 P warps have units in turn.
 template <typename T, int NG, int P>
 __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -428,18 +452,30 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     for (int32_t q = q0 + group; q < q1; q += kGroups) {
       if (!mbar_wait(&codes_full[ring], ring_phase, abort_flag, kWaitBudgetNs, p.status)) break;
       __syncwarp();
-      uint32_t r[2][32 / P];
+      const uint8_t* record = mine + ring * unit_bytes;
+      // Both strips' weights wait in registers for the slot, or with all 128 columns a warp, where the other
+      // groups fill the time, one strip's.
+      constexpr int kHeld = P > 1 ? 2 : 1;
+      uint32_t r[kHeld][32 / P];
+      bool ready = true;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         Part<T, NG, P> strip;
-        strip.load(mine + ring * unit_bytes + j * p.A.record, part, lane, zeros);
-        strip.weights(r[j]);
+        strip.load(record + j * p.A.record, part, lane, zeros);
+        strip.weights(r[j % kHeld]);
+        if (j == kHeld - 1) {
+          ready = mbar_wait(&used[slot], phase, abort_flag, kWaitBudgetNs, p.status);
+          if (!ready) break;
+          __syncwarp();
+          tc_fence_after_sync();
+        }
+        if (P == 1) tmem_store(dst + slot * kUnitTmemCols + (static_cast<uint32_t>(16 * j) << 16), r[0]);
       }
-      if (!mbar_wait(&used[slot], phase, abort_flag, kWaitBudgetNs, p.status)) break;
-      __syncwarp();
-      tc_fence_after_sync();
-      tmem_store(dst + slot * kUnitTmemCols, r[0]);
-      tmem_store(dst + slot * kUnitTmemCols + (16u << 16), r[1]);
+      if (P > 1 && ready) {
+        tmem_store(dst + slot * kUnitTmemCols, r[0]);
+        tmem_store(dst + slot * kUnitTmemCols + (16u << 16), r[kHeld - 1]);
+      }
+      if (!ready) break;
       if (lane == 0) mbar_arrive(&codes_used[ring]);  // all lanes have their weights: the stores are the warp's
       tmem_store_wait();
       tc_fence_before_sync();
@@ -634,11 +670,12 @@ GemmWorkspace layout(int32_t M, int32_t K, int32_t N) {
 
 template <typename T, int NG, int P>
 cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
-  // P = 2: four units between codes and product, two to a group of warps, so one is turned into weights while
-  // the products of the other run.  P = 4, for tiles of which only three fit: all warps on each unit.
-  p.slots = P == 2 ? 4 : 3;
+  // P = 1: four groups of warps have units in turn, each a slot of its own.  P = 4, for tiles of which only three
+  // fit: all warps on each unit.  (Two groups of two ways with two slots each: 34 instead of 32 us for 64 tokens of
+  // 12288^2, for the waits and hand-overs of twice as many warps a unit.)
+  p.slots = P == 1 ? 4 : 3;
   p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * p.n_pad * 256) / (8 * p.A.record))) / 4 *
-           4 * (P == 2) + 3 * (P == 4);
+           4 * (P == 1) + 3 * (P == 4);
   auto kernel = w4_gemm_kernel<T, NG, P>;
   static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
@@ -698,7 +735,7 @@ cudaError_t launch_w4_gemm(const flashspmm_w4* in, const void* B, int64_t ldb, v
   if (e != cudaSuccess) return e;
 
   const int64_t ctas = ctas_of(blocks, p.A.units);
-#define FLASHSPMM_BY_PARTS(T, NG) (p.n_pad <= 128 ? launch_as<T, NG, 2>(p, ctas, s) : launch_as<T, NG, 4>(p, ctas, s))
+#define FLASHSPMM_BY_PARTS(T, NG) (p.n_pad <= 128 ? launch_as<T, NG, 1>(p, ctas, s) : launch_as<T, NG, 4>(p, ctas, s))
 #define FLASHSPMM_BY_GROUP(T)                          \
   e = p.A.group == 128  ? FLASHSPMM_BY_PARTS(T, 1)     \
       : p.A.group == 64 ? FLASHSPMM_BY_PARTS(T, 2)     \

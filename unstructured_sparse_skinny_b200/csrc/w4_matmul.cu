@@ -101,12 +101,12 @@ cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K
 // Eight tokens at a time here, or all at once by tcgen05?  Measured, in us: here
 // 3.5 (6 if the activations have to be copied first) and 0.24 per 1000 records
 // for every eight tokens, 0.3 with groups of 32; there 8.5 (two kernels, the
-// joining of blocks) and 0.3 per 1000 records.
+// joining of blocks) and 0.27 per 1000 records.
 static bool by_fragments(const flashspmm_w4* A, int32_t N, bool aligned) {
   if (N <= 8) return true;
   const double records = 8e-3 * w4_blocks(A->M) * w4_units(A->K);
   const double each = A->group == 32 ? 0.3 : 0.24;
-  return (aligned ? 3.5 : 6.0) + each * ((N + 7) / 8) * records < 8.5 + 0.3 * records;
+  return (aligned ? 3.5 : 6.0) + each * ((N + 7) / 8) * records < 8.5 + 0.27 * records;
 }
 
 size_t w4_matmul_workspace(const flashspmm_w4* A, int32_t N, bool aligned) {

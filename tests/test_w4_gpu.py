@@ -352,3 +352,20 @@ def test_a_layer_runs_on_4_bit_weights_next_to_sparse_ones():
     fs.check_device_status()
     # decoded weights are rounded once (eps / 2), hidden values once (eps / 2) in each, outputs once in each
     assert (y.double() - z.double()).norm() <= 3 * torch.finfo(torch.float16).eps * y.double().norm()
+
+
+@pytest.mark.parametrize("K", [40, 135, 262])
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+def test_rows_that_start_anywhere(K, first):
+    """Views whose rows start on odd values, and their neighbours, which nothing may read into the result."""
+    whole = torch.full((37, K + 8), float("nan"), device="cuda", dtype=torch.bfloat16)
+    W = whole[:, first:first + K]
+    W.copy_(torch.randn((37, K), device="cuda", generator=gen(K)))
+    for symmetric in (True, False):
+        A, B = fs.w4_encode(W, 32, symmetric), fs.w4_encode(W.contiguous(), 32, symmetric)
+        assert torch.equal(A.data, B.data)
+        back = fs.w4_decode(A)
+        assert torch.equal(back.float(), fs.w4_decode(A, torch.float32).bfloat16().float())
+        X = torch.full((20, K + 8), float("nan"), device="cuda", dtype=torch.bfloat16)
+        X[:, first:first + K].copy_(torch.randn((20, K), device="cuda", generator=gen(first)))
+        assert torch.equal(fs.w4_matmul(A, X[:, first:first + K]), fs.w4_matmul(A, X[:, first:first + K].clone()))

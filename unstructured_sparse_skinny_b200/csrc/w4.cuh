@@ -231,6 +231,13 @@ __device__ __forceinline__ uint4 load_act8(const uint16_t* row, int32_t k, int32
   uint4 v = make_uint4(0, 0, 0, 0);
   if (Vec) {
     if (row && k < K) v = *reinterpret_cast<const uint4*>(row + k);
+  } else if (row && k > 0 && k < K - 8) {
+    // inside a row that starts on any value: the four or five words that hold it, which hold no other row's
+    const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + k) >> 1) & 1u;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + k - odd);
+    const uint32_t w[5] = {p[0], p[1], p[2], p[3], odd ? p[4] : 0u};
+    v = make_uint4(__funnelshift_r(w[0], w[1], 16 * odd), __funnelshift_r(w[1], w[2], 16 * odd),
+                   __funnelshift_r(w[2], w[3], 16 * odd), __funnelshift_r(w[3], w[4], 16 * odd));
   } else if (row) {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -250,6 +250,27 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+// On any value's boundary: three words and a fourth, or a value before and one behind them.
+template <typename T>
+__device__ __forceinline__ void store8_any(T* p, const float (&v)[8]) {
+  union {
+    T t[8];
+    uint32_t u[4];
+  } o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o.t[i] = from_float<T>(v[i]);
+  const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 1u;
+  uint32_t* to = reinterpret_cast<uint32_t*>(p + odd);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) to[i] = __funnelshift_r(o.u[i], o.u[i + 1], 16 * odd);
+  if (odd) {
+    p[0] = o.t[0];
+    p[7] = o.t[7];
+  } else {
+    to[3] = o.u[3];
+  }
+}
+__device__ __forceinline__ void store8_any(float*, const float (&)[8]) {}  // four bytes a value: not called
 __device__ __forceinline__ void store1(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
@@ -282,6 +303,8 @@ __global__ void __launch_bounds__(kWarps * 32) w4_decode_kernel(W4Dev A, O* __re
         O* p = W + (at.row + 8 * r) * A.K + k;
         if (Vec) {
           store8(p, v);
+        } else if (sizeof(O) == 2 && k + 8 <= A.K) {
+          store8_any(p, v);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)

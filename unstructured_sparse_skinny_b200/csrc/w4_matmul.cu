@@ -21,7 +21,7 @@ struct MatmulParams {
 // One strip of 16 rows and eight tokens a CTA: its warps have the units in
 // turn and add up at the end.  Codes come two units ahead; the activations,
 // which all CTAs read again, from L1 and L2 as the fragments need them.  What
-// bounds it is turning codes into fragments, 156 instructions a record: one and
+// bounds it is turning codes into fragments, 174 instructions a record: one and
 // eight tokens of 12288^2 take 23 and 25 us, one of 49152 x 12288 71, two thirds
 // of what HBM allows.  (Activations staged in shared memory first delay the
 // short-lived CTAs more than they save, 29 and 54 us; CTAs that stay and read on

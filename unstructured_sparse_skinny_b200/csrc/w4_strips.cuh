@@ -11,8 +11,8 @@
 // four units ahead leave less room for activations, 283).  The activations are
 // staged in shared memory, as many units as fit at a time, and serve all strips
 // of the CTA.  Warps meet only there, and at the end, to add up K.  What bounds
-// it is the rate at which the warps turn codes into fragments: 178 instructions
-// a record, issued in 63 % of the cycles, at half the rate of HBM.  (Sixteen
+// it is the rate at which the warps turn codes into fragments: 177 instructions
+// a record, issued in 65 % of the cycles, at half the rate of HBM.  (Sixteen
 // warps with one strip each read the activations twice as often: a fifth slower.)
 //
 // A group's weights enter the product as whole numbers q - z, and the fp32 sum

@@ -1,5 +1,5 @@
-// 4-bit weights with group scales: layout, launchers and the warp-level
-// product shared by the skinny matrix product and the experts' products.
+// 4-bit weights with group scales: layout, fragments and launchers, shared by
+// the skinny matrix product and the experts' products.
 //
 // Layout.  A matrix of M x K codes is cut into strips of 16 rows, eight strips
 // to a block of 128, and units of 128 columns.  A unit of one strip is one
@@ -284,55 +284,6 @@ struct W4Groups {
   }
   __device__ __forceinline__ W4Zero<T> zero(int i) const { return W4Zero<T>(zero_point(i, 0), zero_point(i, 1)); }
 };
-
-// One unit of R strips times NT * 8 activation rows: acc[r][nt] += s * ((q - z) x B).
-// `act(nt, k)` gives the lane's 16 bytes of activations k .. k + 7 of row
-// 8 * nt + g (zeros where there is none); tiles from `tiles` on are skipped.
-// A group is multiplied as whole numbers q - z and scaled in fp32 afterwards,
-// so a weight is never rounded.
-template <typename T, int NG, int R, int NT, typename Act>
-__device__ __forceinline__ void w4_unit(const uint4 (&c)[R][2], const W4Groups<T, NG> (&grp)[R], int32_t k0, int tiles,
-                                        const Act& act, float (&acc)[R][NT][4]) {
-  constexpr int kBlocks = 4 / NG;
-#pragma unroll
-  for (int gi = 0; gi < NG; ++gi) {
-    uint32_t a[R][2 * kBlocks][4];
-    float s0[R], s1[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const W4Zero<T> z = grp[r].zero(gi);
-      s0[r] = grp[r].scale(gi, 0);
-      s1[r] = grp[r].scale(gi, 1);
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const int blk = gi * kBlocks + b;
-        const uint4 v = c[r][blk >> 1];
-        w4_fragment(blk & 1 ? v.z : v.x, z, a[r][2 * b]);
-        w4_fragment(blk & 1 ? v.w : v.y, z, a[r][2 * b + 1]);
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt >= tiles) break;
-      uint4 x[kBlocks];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) x[b] = act(nt, k0 + 32 * (gi * kBlocks + b));
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          mma16816<T>(d, a[r][2 * b], x[b].x, x[b].y);
-          mma16816<T>(d, a[r][2 * b + 1], x[b].z, x[b].w);
-        }
-        acc[r][nt][0] = fmaf(s0[r], d[0], acc[r][nt][0]);
-        acc[r][nt][1] = fmaf(s0[r], d[1], acc[r][nt][1]);
-        acc[r][nt][2] = fmaf(s1[r], d[2], acc[r][nt][2]);
-        acc[r][nt][3] = fmaf(s1[r], d[3], acc[r][nt][3]);
-      }
-    }
-  }
-}
 
 // ---------------------------------------------------------------- launchers
 

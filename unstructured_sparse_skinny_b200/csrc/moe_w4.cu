@@ -524,9 +524,10 @@ __global__ void __launch_bounds__(kStripThreads, strip_ctas(NT)) moe_down_kernel
 
 // Up to eight tokens: a CTA has a pair of strips of the output and all running
 // experts, whose units its warps share in runs.  A token is a column of the
-// product (zeros where the expert is not its choice), so a warp adds an expert's
-// weighted sums in registers and the CTA its warps', and no partial result
-// leaves the SM.
+// product, so a warp adds an expert's weighted sums in registers and the CTA its
+// warps', and no partial result leaves the SM.  Where the expert is not a
+// token's choice the column's activations are zeros and its sum is not added: a
+// scale that is not finite makes it NaN.
 constexpr int kDirectWarps = 16, kDirectSlots = kDirectTokens * kMoeMaxTopK;
 
 template <typename T, int NG>
@@ -630,7 +631,8 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          total[r][k] = fmaf(weight[s][2 * t + (k & 1)], acc[r][0][k], total[r][k]);
+          const int n = 2 * t + (k & 1);
+          if (slots[s].tokens >> n & 1) total[r][k] = fmaf(weight[s][n], acc[r][0][k], total[r][k]);
           acc[r][0][k] = 0.0f;
         }
       u = 0;

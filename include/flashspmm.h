@@ -414,7 +414,7 @@ size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B,
 
 /* Skinny product C = A x B with fp32 sums.  Up to N = 8 the sums are of s times
  * whole numbers q - z; above, a weight s * (q - z) may be rounded to A->dtype
- * first, as flashspmm_w4_decode gives it.
+ * first, as flashspmm_w4_decode gives it: the sizes decide, not where B lies.
  *   A          a view with count = 1.
  *   B          device, A->dtype, N rows of K activations, ldb values apart
  *              (any alignment; rows that start on 16 bytes with K % 8 == 0 are

@@ -25,3 +25,116 @@ def test_the_same_bits_wherever_the_activations_lie(M, K, N, group):
     wide = torch.zeros((N, K + 3), device="cuda", dtype=torch.bfloat16)
     wide[:, 1:1 + K] = B
     assert torch.equal(fs.w4_matmul(A, wide[:, 1:1 + K]), want)
+
+
+def check(got, W, B, rounded_weights):
+    """Bound of one output: (K / 16 + 64) * 2^-23 * sum |w x| for the sums, as in test_w4_gpu.py, eps / 2 of sum |w x|
+    where weights are rounded to 16 bits, eps / 2 of the value for a 16-bit output and half its smallest step."""
+    want, size = B.double() @ W.t(), B.double().abs() @ W.abs().t()
+    eps, K = torch.finfo(B.dtype).eps, W.shape[1]
+    bound = (K / 16 + 64) * 2.0 ** -23 * size
+    if rounded_weights:
+        bound += eps / 2 * size
+    if got.dtype is not torch.float32:
+        bound += eps / 2 * (want.abs() + bound) + torch.finfo(B.dtype).smallest_normal * eps
+    off = (got.double() - want).abs()
+    assert (off <= bound).all(), f"{(off / bound).max().item():.3g} of the bound"
+    # Roundings of weights are independent: over a row of K they add up like their root of squares, and a whole result
+    # is no further off than one rounding of the output (eps / 2) and one of the weights (eps / 2).
+    assert off.norm() <= (eps + 1e-6) * want.norm()
+
+
+M, K = 2600, 8200  # 21 blocks of 65 units: shared and whole blocks, a last block of 40 rows and a last unit of 8 columns
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("N", [33, 64, 65, 100, 128, 129, 200, 256])
+def test_tensor_memory_kernel(dtype, group, symmetric, N):
+    codes, scales, zeros = codes_of((M, K), group, dtype, symmetric, N)
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    assert on_tensor_memory(A, N)
+    B = torch.randn((N, K), device="cuda", generator=gen(N)).to(dtype)
+    check(fs.w4_matmul(A, B), dense64(codes, scales, zeros, group), B, True)
+
+
+@pytest.mark.parametrize("group,symmetric", [(32, False), (64, True), (128, False)])
+@pytest.mark.parametrize("rows,columns,N", [(129, 65536, 40), (12288, 1032, 100), (40000, 136, 70), (128, 33000, 256),
+                                            (4099, 5008, 17), (12288, 4104, 12)])
+def test_tensor_memory_kernel_shapes(rows, columns, N, group, symmetric):
+    """Few rows and many columns, the other way round, and the fewest tokens that go there."""
+    codes, scales, zeros = codes_of((rows, columns), group, torch.bfloat16, symmetric, N)
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    B = torch.randn((N, columns), device="cuda", generator=gen(N)).bfloat16()
+    check(fs.w4_matmul(A, B), dense64(codes, scales, zeros, group), B, on_tensor_memory(A, N))
+
+
+@pytest.mark.parametrize("N", [40, 140])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_tensor_memory_kernel_strides(N, group):
+    codes, scales, zeros = codes_of((M, K), group, torch.float16, False, 2)
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    assert on_tensor_memory(A, N)
+    B = torch.randn((N, K), device="cuda", generator=gen(1)).half()
+    want = fs.w4_matmul(A, B)
+    for pitch, first in ((K + 8, 8), (K + 3, 1), (K + 1, 0), (K + 5, 5)):
+        wide = torch.full((N, pitch), float("nan"), device="cuda", dtype=torch.float16)
+        wide[:, first:first + K] = B
+        assert torch.equal(fs.w4_matmul(A, wide[:, first:first + K]), want)
+    assert torch.equal(fs.w4_matmul(A, B[:1].expand(N, K)), want[:1].expand(N, M))
+    wide = torch.full((N + 2, M + 9), 5.0, device="cuda", dtype=torch.float16)
+    fs.w4_matmul(A, B, wide[1:N + 1, 4:4 + M])
+    assert torch.equal(wide[1:N + 1, 4:4 + M], want)
+    wide[1:N + 1, 4:4 + M] = 5
+    assert (wide == 5).all()
+
+
+@pytest.mark.parametrize("N", [40, 140])
+@pytest.mark.parametrize("group", [32, 128])
+def test_tensor_memory_kernel_non_finite_activations(N, group):
+    codes, scales, zeros = codes_of((M, K), group, torch.float16, True, 2)
+    codes[:, 5] = 9  # no weight of column 5 is zero
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    assert on_tensor_memory(A, N)
+    B = torch.randn((N, K), device="cuda", generator=gen(1)).half()
+    want = fs.w4_matmul(A, B)
+    for value in (float("inf"), -float("inf"), float("nan")):
+        B[N - 1, 5] = value
+        got = fs.w4_matmul(A, B)
+        assert torch.equal(got[:-1], want[:-1])
+        assert torch.isnan(got[-1]).all() if value != value else (got[-1] == value).all()
+
+
+@pytest.mark.parametrize("N", [40, 140])
+def test_tensor_memory_kernel_non_finite_scales(N):
+    """A row with a scale that is not finite is not finite, and the others are as they were."""
+    codes, scales, zeros = codes_of((M, K), 64, torch.bfloat16, False, 2)
+    B = torch.randn((N, K), device="cuda", generator=gen(1)).bfloat16()
+    want = fs.w4_matmul(fs.w4_pack(codes, scales, zeros, group=64), B)
+    scales[77, 3], scales[2590, 128] = float("inf"), float("nan")
+    got = fs.w4_matmul(fs.w4_pack(codes, scales, zeros, group=64), B)
+    assert not torch.isfinite(got[:, [77, 2590]]).any()
+    got[:, [77, 2590]] = want[:, [77, 2590]]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("N", [40, 140])
+@pytest.mark.parametrize("group", [32, 128])
+def test_tensor_memory_kernel_in_graphs_and_streams(N, group):
+    """A captured call and eager ones, on two streams, at once."""
+    codes, scales, zeros = codes_of((M, K), group, torch.bfloat16, False, 2)
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    assert on_tensor_memory(A, N)
+    Bs = [torch.randn((N, K), device="cuda", generator=gen(i)).bfloat16() for i in range(3)]
+    want = [fs.w4_matmul(A, b) for b in Bs]
+    x, graph, side = Bs[0].clone(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        out = fs.w4_matmul(A, x)
+    for i in (1, 2, 0):
+        x.copy_(Bs[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        other = [fs.w4_matmul(A, b, stream=side) for b in Bs]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]) and all(torch.equal(a, b) for a, b in zip(other, want))

@@ -529,6 +529,7 @@ __global__ void __launch_bounds__(kStripThreads, strip_ctas(NT)) moe_down_kernel
 // token's choice the column's activations are zeros and its sum is not added: a
 // scale that is not finite makes it NaN.
 constexpr int kDirectWarps = 16, kDirectSlots = kDirectTokens * kMoeMaxTopK;
+constexpr uint32_t kNotChosen = 0x80000000u;  // -0 for a weight: a choice's own is made +0
 
 template <typename T, int NG>
 __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(const ExpertParams p,
@@ -546,8 +547,8 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
     const Slot s = p.ws.slots[i >> 3];
     const int n = i & 7;
     if (n == 0) slots[i >> 3] = s;
-    weight[i >> 3][n] =
-        s.tokens >> n & 1 ? p.ws.pair_weight[s.first + __popc(s.tokens & ((1u << n) - 1))] : 0.0f;
+    weight[i >> 3][n] = s.tokens >> n & 1 ? p.ws.pair_weight[s.first + __popc(s.tokens & ((1u << n) - 1))] + 0.0f
+                                          : __uint_as_float(kNotChosen);
   }
   __syncthreads();
   const int64_t items = static_cast<int64_t>(running) * units;
@@ -631,8 +632,8 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int n = 2 * t + (k & 1);
-          if (slots[s].tokens >> n & 1) total[r][k] = fmaf(weight[s][n], acc[r][0][k], total[r][k]);
+          const float w = weight[s][2 * t + (k & 1)];
+          if (__float_as_uint(w) != kNotChosen) total[r][k] = fmaf(w, acc[r][0][k], total[r][k]);
           acc[r][0][k] = 0.0f;
         }
       u = 0;

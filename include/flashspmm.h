@@ -449,9 +449,9 @@ size_t flashspmm_moe_w4_workspace_bytes(const flashspmm_w4* gate, const void* X,
  *   X          device, dtype, `tokens` rows of H, ldx values apart (alignment
  *              as in flashspmm_w4_matmul).
  *   router     device, E x H row-major, dtype or FLASHSPMM_F32 (router_dtype).
- *              Logits are summed in some 46 bits, so the choice does not depend
- *              on the order of a sum.  A NaN logit is chosen last and its
- *              token's p are NaN.
+ *              Logits are summed in some 46 bits; two that are closer than that
+ *              may come out in either order, equal rows of the router are a tie.
+ *              A NaN logit is chosen last and its token's p are NaN.
  *              NULL: ids and weights are inputs, a routing of the caller's.
  *              An id outside 0 .. E - 1 contributes nothing, one named twice
  *              by a token counts with the sum of its weights.

@@ -111,11 +111,14 @@ struct RouterRow<float> {
 // computed (Knuth's two-sum) and added up beside.  64-bit arithmetic would do,
 // but the conversions to it run at some 5 a cycle and SM: 17 us for one token
 // and 128 experts of 2048 columns on a cluster, where this takes 3.
+// (Every step is an intrinsic: an expression the compiler could turn into a fused
+// multiply-add, which leaves no rounding to compute.)
 struct Sum2 {
   float s = 0.0f, c = 0.0f;
   __device__ __forceinline__ void add(float p, float below) {
-    const float t = s + p, z = t - s;
-    c += ((s - (t - z)) + (p - z)) + below;
+    const float t = __fadd_rn(s, p), z = __fsub_rn(t, s);
+    const float left = __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z));
+    c = __fadd_rn(c, __fadd_rn(left, below));
     s = t;
   }
   // of an infinite sum the rounding is not a number, and not wanted
@@ -126,8 +129,8 @@ struct Sum2 {
 // w * x: a product of two 16-bit values is exact in fp32, of an fp32 router's its rounding is kept.
 template <typename RT>
 __device__ __forceinline__ void add_product(Sum2& sum, float w, float x) {
-  const float p = w * x;
-  sum.add(p, std::is_same<RT, float>::value ? fmaf(w, x, -p) : 0.0f);
+  const float p = __fmul_rn(w, x);
+  sum.add(p, std::is_same<RT, float>::value ? __fmaf_rn(w, x, -p) : 0.0f);
 }
 
 // A CTA has EB experts and TB tokens; its threads share the columns, eight

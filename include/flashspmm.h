@@ -364,7 +364,8 @@ enum { FLASHSPMM_ACT_SILU = 0, FLASHSPMM_ACT_GELU = 1, FLASHSPMM_ACT_RELU = 2 };
  * flashspmm_w4_encode or flashspmm_w4_pack.
  *
  * Layout: blocks of 128 rows (eight strips of 16) times units of 128 columns,
- * both padded with zero weights.  The unit of one strip is a record of 1024
+ * both padded: rows with zero weights, columns with the codes nearest to the zero
+ * points (zero weights up to z = 15).  The unit of one strip is a record of 1024
  * bytes of codes, 32 * (128 / group) bytes of scales and, with zero points,
  * 16 * (128 / group) bytes of them; it is the (((matrix * ceil(M/128) + block) *
  * ceil(K/128) + unit) * 8 + strip)-th record.  Codes are ordered so that lane

@@ -180,7 +180,10 @@ __global__ void __launch_bounds__(kWarps * 32) w4_encode_kernel(const uint16_t* 
 }
 
 // Codes of one byte each ([count * M][K]) with scales and zero points
-// [count * M][ceil(K / group)] to the layout.  Padding decodes to zero.
+// [count * M][ceil(K / group)] to the layout.  A group's columns behind K get the
+// code nearest to its zero point: a zero weight, or where the point is above 15
+// the smallest that the group can have, so they overflow 16 bits only if all of
+// its weights do.  (The activations that meet them are zeros.)
 template <int NG, bool Vec>
 __global__ void __launch_bounds__(kWarps * 32) w4_pack_kernel(const uint8_t* __restrict__ in,
                                                               const uint16_t* __restrict__ in_scales,
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32) w4_pack_kernel(const uint8_t* __r
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const bool ok = r ? at.ok1 : at.ok0;
-        const uint32_t pad = zp[r][b * NG / 4] & 0xF;
+        const uint32_t pad = min(zp[r][b * NG / 4], 15u);
         const uint8_t* p = in + (at.row + 8 * r) * A.K + k;
         if (Vec) {
           uint2 v = make_uint2(pad * 0x01010101u, pad * 0x01010101u);

@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kStripThreads, strip_ctas(NT)) moe_gate_up_ker
       *h = rounded;
       h[p.rest] = from_float<T>(isfinite(left) ? left : 0.0f);  // of an h that rounds to infinity: nothing
     };
-    strip_reduce<NT>(acc, p.pairs, rows, staged, [&](int i, int32_t n, int32_t row, float a, float b) {
+    strip_reduce<T, NT>(acc, p.pairs, rows, staged, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t f = (pair0 + i) * (Gated ? 16 : 32) + row;
       a = activate(p.activation, a);
       store(n, f, Gated ? a * b : a);
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kStripThreads, strip_ctas(NT)) moe_down_kernel
         at, A.units, static_cast<int32_t>(p.ws.ldh), rows, p.pairs, smem, staged, p.shared - rings,
         [&](int32_t n) { return p.ws.h + (n < rows ? first + n : first + n - rows) * p.ws.ldh + (n < rows ? 0 : p.rest); },
         acc);
-    strip_reduce<NT>(acc, p.pairs, rows, staged, [&](int i, int32_t n, int32_t row, float a, float b) {
+    strip_reduce<T, NT>(acc, p.pairs, rows, staged, [&](int i, int32_t n, int32_t row, float a, float b) {
       const int32_t m = (pair0 + i) * 32 + row;
       const float w = p.ws.pair_weight[first + n];
       float* y = p.ws.y + static_cast<int64_t>(first + n) * A.M;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) moe_down_direct_kernel(c
 #pragma unroll
     for (int w = 0; w < kDirectWarps; ++w) sum += red[w][n][r];
     const int32_t m = blockIdx.x * 32 + r;
-    if (n < p.tokens && m < A.M) out[n * ldo + m] = from_float<T>(sum);
+    if (n < p.tokens && m < A.M) out[n * ldo + m] = from_float<T>(w4_raise<T>(sum));
   }
 }
 

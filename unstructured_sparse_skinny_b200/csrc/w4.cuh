@@ -111,30 +111,47 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
+// Fragments for sums of whole numbers times activations hold q - z, in bf16
+// (q - z) 2^-13, exact like it: |q - z| <= 63, so a group's sum of 128 products
+// stays below the largest fp32 value whatever bf16 activations it has, and what
+// is scaled and added up is infinite only if the result nearly is.  The finished
+// sum is multiplied by w4_raise.  At the other end sums are kept to 2^-136
+// instead of 2^-149.  (fp16 activations are below 2^16.)
+template <typename T>
+constexpr int kW4Down = 0;  // binary orders
+template <>
+constexpr int kW4Down<__nv_bfloat16> = 13;
+template <typename T>
+__device__ __forceinline__ float w4_raise(float sum) {
+  return kW4Down<T> ? sum * static_cast<float>(1 << kW4Down<T>) : sum;
+}
+
 // The pair {z, z} (first row) and its like for the second row, in the form
 // that w4_fragment subtracts.
-template <typename T>
+template <typename T, int Down>
 struct W4Zero;
 template <>
-struct W4Zero<__half> {
+struct W4Zero<__half, 0> {
   __half2 lo, hi;  // 1024 + z, -(64 + z'), put together as bits: steps there are 1 and 1/16, and z < 64
   __device__ __forceinline__ W4Zero(int z0, int z1)
       : lo(__half2half2(__ushort_as_half(static_cast<uint16_t>(0x6400 | z0)))),
         hi(__half2half2(__ushort_as_half(static_cast<uint16_t>(0xD400 | (z1 << 4))))) {}
 };
-template <>
-struct W4Zero<__nv_bfloat16> {
-  __nv_bfloat162 lo, hi;  // 128 + z, 128 + z'
+template <int Down>
+struct W4Zero<__nv_bfloat16, Down> {
+  static constexpr uint32_t kBase = 0x4300 - (Down << 7);  // 128 * 2^-Down
+  __nv_bfloat162 lo, hi;                                    // (128 + z) * 2^-Down, (128 + z') * 2^-Down
   __device__ __forceinline__ W4Zero(int z0, int z1)
-      : lo(__bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(0x4300 | z0)))),
-        hi(__bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(0x4300 | z1)))) {}
+      : lo(__bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(kBase | z0)))),
+        hi(__bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(kBase | z1)))) {}
 };
 
-// Eight codes of one word to the fragment q - z, exact: a nibble put under the
-// bits of 1024 is 1024 + q (fp16, nibbles 0 and 4) or 1024 + 16 q (nibbles 1
-// and 5), and the subtraction, or the fused multiply by 1/16 and subtraction,
-// rounds nothing.  bf16 has 7 mantissa bits: a nibble under 128 is 128 + q.
-__device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__half>& z, uint32_t (&a)[4]) {
+// Eight codes of one word to the fragment (q - z) 2^-Down, exact: a nibble put
+// under the bits of 1024 is 1024 + q (fp16, nibbles 0 and 4) or 1024 + 16 q
+// (nibbles 1 and 5), and the subtraction, or the fused multiply by 1/16 and
+// subtraction, rounds nothing.  bf16 has 7 mantissa bits: a nibble under 128 is
+// 128 + q, and likewise at every other power of two.
+__device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__half, 0>& z, uint32_t (&a)[4]) {
   const uint32_t base = 0x64006400u;
   const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));
   const uint32_t v = w >> 8;
@@ -155,8 +172,9 @@ __device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__half>& z,
   x.h = __hfma2(x.h, sixteenth, z.hi);
   a[3] = x.u;
 }
-__device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__nv_bfloat16>& z, uint32_t (&a)[4]) {
-  const uint32_t base = 0x43004300u;
+template <int Down>
+__device__ __forceinline__ void w4_fragment(uint32_t w, const W4Zero<__nv_bfloat16, Down>& z, uint32_t (&a)[4]) {
+  const uint32_t base = z.kBase * 0x10001u;
   union U {
     uint32_t u;
     __nv_bfloat162 h;
@@ -282,7 +300,7 @@ struct W4Groups {
   __device__ __forceinline__ int zero_point(int i, int row) const {
     return static_cast<int>(z[i >> 1] >> (16 * (i & 1) + 8 * row) & 0xFF);
   }
-  __device__ __forceinline__ W4Zero<T> zero(int i) const { return W4Zero<T>(zero_point(i, 0), zero_point(i, 1)); }
+  __device__ __forceinline__ W4Zero<T, kW4Down<T>> zero(int i) const { return {zero_point(i, 0), zero_point(i, 1)}; }
 };
 
 // ---------------------------------------------------------------- launchers

@@ -215,7 +215,7 @@ struct Part {
   __device__ __forceinline__ void weights(uint32_t (&r)[4 * kWords]) const {
 #pragma unroll
     for (int gi = 0; gi < kGroups; ++gi) {
-      const W4Zero<T> zero(static_cast<int>(z[gi] & 0xFF), static_cast<int>(z[gi] >> 8));
+      const W4Zero<T, 0> zero(static_cast<int>(z[gi] & 0xFF), static_cast<int>(z[gi] >> 8));
       const uint32_t s0 = __byte_perm(s[gi], 0, 0x1010), s1 = __byte_perm(s[gi], 0, 0x3232);
 #pragma unroll
       for (int i = gi * kWords / kGroups; i < (gi + 1) * kWords / kGroups; ++i) {

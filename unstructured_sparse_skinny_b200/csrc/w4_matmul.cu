@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kMatmulWarps * 32, 2) w4_matmul_kernel(const M
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kMatmulWarps; ++w) sum += red[w][i][r];
+    sum = w4_raise<T>(sum);
     const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + r;
     if (n < p.N && m < p.A.M) {
       if (p.c_f32)

@@ -15,8 +15,8 @@
 // a record, issued in 65 % of the cycles, at half the rate of HBM.  (Sixteen
 // warps with one strip each read the activations twice as often: a fifth slower.)
 //
-// A group's weights enter the product as whole numbers q - z, and the fp32 sum
-// of the group is scaled: no weight is rounded.
+// A group's weights enter the product as whole numbers q - z (in bf16 times a
+// power of two), and the fp32 sum of the group is scaled: no weight is rounded.
 #pragma once
 
 #include <cmath>
@@ -60,9 +60,10 @@ struct StripUnit {
   }
 };
 
-// acc += the unit's product with activations, of R strips; x(nt, b, part) gives
-// the lane's 16 bytes of its row of tile nt and the unit's 32-column block b.
-// Activations of several parts are their sum.
+// acc += the unit's product with activations, of R strips (w4_raise of a finished
+// acc is the product); x(nt, b, part) gives the lane's 16 bytes of its row of
+// tile nt and the unit's 32-column block b.  Activations of several parts are
+// their sum.
 template <typename T, int NG, int R, int NT, int Tiles, int Parts = 1, typename Act>
 __device__ __forceinline__ void strip_unit(const StripUnit<T, NG> (&unit)[R], int tiles, const Act& x,
                                            float (&acc)[R][Tiles][4]) {
@@ -76,7 +77,7 @@ __device__ __forceinline__ void strip_unit(const StripUnit<T, NG> (&unit)[R], in
       uint32_t a[R][2][4];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const W4Zero<T> z = unit[r].g.zero(gi);
+        const auto z = unit[r].g.zero(gi);
         w4_fragment(unit[r].word(2 * blk), z, a[r][0]);
         w4_fragment(unit[r].word(2 * blk + 1), z, a[r][1]);
       }
@@ -230,7 +231,7 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
 }
 
 // Adds the warps' shares of K: out(pair, n, row, sum of the first strip, of the second).
-template <int NT, typename Out>
+template <typename T, int NT, typename Out>
 __device__ __forceinline__ void strip_reduce(const float (&acc)[2][NT][4], int pairs, int32_t rows, uint8_t* smem,
                                              const Out& out) {
   constexpr int kPitch = 36;  // 32 rows, and the fragments' stores meet all banks
@@ -252,7 +253,7 @@ __device__ __forceinline__ void strip_reduce(const float (&acc)[2][NT][4], int p
       a += red[(w * NT * 8 + n) * kPitch + m];
       b += red[(w * NT * 8 + n) * kPitch + 16 + m];
     }
-    out(pair, n, m, a, b);
+    out(pair, n, m, w4_raise<T>(a), w4_raise<T>(b));
   }
 }
 

@@ -17,7 +17,7 @@ grad is refused while grad mode is on.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass, field
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -32,9 +32,23 @@ class _W4View(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("zeros", ctypes.c_int32), ("data", ctypes.c_void_p)]
 
 
+def _shape(count: int, M: int, K: int, group: int, symmetric: bool) -> tuple:
+    """Shape of the data of ``count`` matrices."""
+    nbytes = binding.load_library().flashspmm_w4_bytes(M, K, count, group, int(not symmetric))
+    if nbytes < 0:
+        raise ValueError(f"4-bit weights need group 32, 64 or 128 and at least one matrix, got group {group}, "
+                         f"{count} of {M} x {K}")
+    blocks, units = -(-M // 128), -(-K // 128)
+    return count, blocks, units, 8, nbytes // max(1, count * blocks * units * 8)
+
+
 @dataclass(frozen=True, eq=False)
 class W4:
-    """A 4-bit matrix [M, K], or a stack [count, M, K], in device memory."""
+    """A 4-bit matrix [M, K], or a stack [count, M, K], in device memory.
+
+    It can be copied, pickled and saved.  Data in host memory, as a file loaded
+    without a GPU leaves them, can be held but not multiplied;
+    ``dataclasses.replace(A, data=A.data.cuda())`` moves them."""
     data: torch.Tensor   # uint8 [count, blocks, units, 8, record]: blocks of 128 rows, units of 128 columns
     dtype: torch.dtype   # of the scales, and of the activations they meet: float16 or bfloat16
     M: int
@@ -42,12 +56,31 @@ class W4:
     group: int
     symmetric: bool      # without zero points: every one is 8
     stacked: bool = False  # made from a 3-D tensor
-    _ref: object = field(default=None, init=False, repr=False)
 
     def __post_init__(self):
-        v = _W4View(self.M, self.K, self.data.shape[0], self.group, _DTYPES[self.dtype], int(not self.symmetric),
+        if not isinstance(self.data, torch.Tensor) or self.data.dtype is not torch.uint8 or \
+                self.data.device.type not in ("cuda", "cpu"):
+            raise TypeError("data must be a uint8 tensor")
+        if self.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("dtype must be torch.float16 or torch.bfloat16")
+        count = self.data.shape[0] if self.data.dim() else 0
+        shape = _shape(count, self.M, self.K, self.group, self.symmetric)
+        if tuple(self.data.shape) != shape or not self.data.is_contiguous() or self.data.data_ptr() % 16 != 0 or \
+                (count != 1 and not self.stacked):
+            raise ValueError(f"data must be a contiguous {list(shape)} tensor on a 16-byte boundary, "
+                             f"got {list(self.data.shape)}")
+        # the kernels' view: byref keeps the structure alive, and a copy makes its own
+        v = _W4View(self.M, self.K, count, self.group, _DTYPES[self.dtype], int(not self.symmetric),
                     self.data.data_ptr() or None)
-        object.__setattr__(self, "_ref", ctypes.byref(v))  # byref keeps the structure alive
+        object.__setattr__(self, "_ref", ctypes.byref(v))
+
+    def __getstate__(self):
+        return {f.name: getattr(self, f.name) for f in fields(self)}
+
+    def __setstate__(self, state):
+        for name, value in state.items():
+            object.__setattr__(self, name, value)
+        self.__post_init__()
 
     @property
     def count(self) -> int:
@@ -89,6 +122,8 @@ class _On:
 
 
 def _elsewhere(device: torch.device, stream) -> bool:
+    if device.index is None:  # host memory
+        raise TypeError(f"4-bit weights are multiplied on a GPU, these are on {device}")
     return stream is not None or torch.cuda.current_device() != device.index
 
 
@@ -133,13 +168,7 @@ def _output(t, shape: tuple, dtypes, device: torch.device, name: str) -> int:
 def _empty(shape, dtype: torch.dtype, group: int, symmetric: bool, device: torch.device) -> W4:
     """Unwritten data for a weight of shape [M, K] or [count, M, K]."""
     count, (M, K) = (shape[0] if len(shape) == 3 else 1), shape[-2:]
-    nbytes = binding.load_library().flashspmm_w4_bytes(M, K, count, group, int(not symmetric))
-    if nbytes < 0:
-        raise ValueError(f"4-bit weights need group 32, 64 or 128 and at least one matrix, got group {group}, "
-                         f"shape {tuple(shape)}")
-    blocks, units = -(-M // 128), -(-K // 128)
-    record = nbytes // max(1, count * blocks * units * 8)
-    return W4(torch.empty((count, blocks, units, 8, record), dtype=torch.uint8, device=device), dtype, M, K, group,
+    return W4(torch.empty(_shape(count, M, K, group, symmetric), dtype=torch.uint8, device=device), dtype, M, K, group,
               symmetric, len(shape) == 3)
 
 

@@ -382,7 +382,8 @@ typedef struct {
   void* data;     /* device, 16-byte aligned */
 } flashspmm_w4;
 
-/* Bytes of data that a view of these sizes holds; -1 on bad arguments. */
+/* Bytes of data that a view of these sizes holds; -1 on bad arguments, or if 63
+ * bits do not hold them. */
 int64_t flashspmm_w4_bytes(int32_t M, int32_t K, int32_t count, int32_t group, int32_t zeros);
 
 /* Encoder: a dense weight to A's data.

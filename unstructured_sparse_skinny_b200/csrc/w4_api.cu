@@ -24,11 +24,19 @@ flashspmm_status check_shape(int32_t M, int32_t K, int32_t count, int32_t group)
   return FLASHSPMM_OK;
 }
 
+// -1 if 64 bits do not hold it.
+int64_t data_bytes(int32_t M, int32_t K, int32_t count, int32_t group, bool zeros) {
+  const int64_t one = static_cast<int64_t>(w4_blocks(M)) * 8 * w4_units(K) * w4_record_bytes(kW4UnitCols / group, zeros);
+  int64_t all = 0;
+  return __builtin_mul_overflow(one, static_cast<int64_t>(count), &all) ? -1 : all;
+}
+
 flashspmm_status check_w4(const flashspmm_w4* A) {
   if (!A || A->zeros < 0 || A->zeros > 1) return FLASHSPMM_ERR_INVALID_ARG;
   const flashspmm_status st = check_shape(A->M, A->K, A->count, A->group);
   if (st != FLASHSPMM_OK) return st;
   if (A->dtype != FLASHSPMM_F16 && A->dtype != FLASHSPMM_BF16) return FLASHSPMM_ERR_UNSUPPORTED;
+  if (data_bytes(A->M, A->K, A->count, A->group, A->zeros != 0) < 0) return FLASHSPMM_ERR_UNSUPPORTED;
   if (A->M > 0 && A->K > 0 && !A->data) return FLASHSPMM_ERR_INVALID_ARG;
   if (!aligned16(A->data)) return FLASHSPMM_ERR_ALIGNMENT;
   return FLASHSPMM_OK;
@@ -43,7 +51,7 @@ extern "C" {
 
 int64_t flashspmm_w4_bytes(int32_t M, int32_t K, int32_t count, int32_t group, int32_t zeros) {
   if (check_shape(M, K, count, group) != FLASHSPMM_OK || zeros < 0 || zeros > 1) return -1;
-  return static_cast<int64_t>(count) * w4_blocks(M) * 8 * w4_units(K) * w4_record_bytes(kW4UnitCols / group, zeros != 0);
+  return data_bytes(M, K, count, group, zeros != 0);
 }
 
 flashspmm_status flashspmm_w4_encode(const void* W, int64_t ldw, int32_t symmetric, const flashspmm_w4* A,

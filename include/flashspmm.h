@@ -423,6 +423,7 @@ size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B,
  *              read as they are, others are copied to the workspace first).
  *   C          device, c_dtype = A->dtype or FLASHSPMM_F32, N rows of M values,
  *              ldc values apart.  Nothing between the rows is written.
+ *              C must not overlap B: some rows are written while B is read.
  *   N          1 .. 256.
  *   workspace  device, 16-byte aligned, flashspmm_w4_matmul_workspace_bytes;
  *              needs no initialisation.  Calls that may run concurrently need
@@ -460,7 +461,7 @@ size_t flashspmm_moe_w4_workspace_bytes(const flashspmm_w4* gate, const void* X,
  *   ids        device int32[tokens][top_k];  weights  device float[tokens][top_k]:
  *              outputs with a router, inputs without.
  *   out        device, dtype, `tokens` rows of H, ldo values apart.  A token
- *              that no expert takes gets zeros.
+ *              that no expert takes gets zeros.  May be X itself.
  *   tokens     0 .. 64;  E <= 512;  top_k 1 .. 16 (<= E with a router).
  *   workspace  device, 16-byte aligned; needs no initialisation.  Calls that
  *              may run concurrently need separate ones.

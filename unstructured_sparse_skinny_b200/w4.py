@@ -32,6 +32,19 @@ class _W4View(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("zeros", ctypes.c_int32), ("data", ctypes.c_void_p)]
 
 
+def _overlap(a: torch.Tensor, lda: int, b: torch.Tensor, ldb: int) -> bool:
+    """Whether rows of a and of b (as many; their distances in values) share memory, to be safe also where only their
+    ranges meet, unless equal distances keep their columns apart."""
+    rows, (wa, wb) = a.shape[0], (t.shape[1] * t.element_size() for t in (a, b))
+    if rows == 0 or wa == 0 or wb == 0:
+        return False
+    pa, pb, at, bt = lda * a.element_size(), ldb * b.element_size(), a.data_ptr(), b.data_ptr()
+    if at >= bt + (rows - 1) * pb + wb or bt >= at + (rows - 1) * pa + wa:
+        return False
+    apart = (bt - at) % pa if pa == pb else 0
+    return rows == 1 or not (wa <= apart <= pa - wb)
+
+
 def _shape(count: int, M: int, K: int, group: int, symmetric: bool) -> tuple:
     """Shape of the data of ``count`` matrices."""
     nbytes = binding.load_library().flashspmm_w4_bytes(M, K, count, group, int(not symmetric))
@@ -239,7 +252,7 @@ def w4_decode(A: W4, dtype: torch.dtype | None = None, stream=None) -> torch.Ten
 def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """C = A x B for a skinny B.  B is ``[N, K]`` in A's type with N = 1..256
     (rows may be apart); returns C as ``[N, M]`` in that type, or writes the
-    given C, which may be float32 (the unrounded sums)."""
+    given C, which may be float32 (the unrounded sums) and must not overlap B."""
     lib = binding._lib or binding.load_library()
     device, dtype = A.data.device, A.dtype
     if B.dtype is not dtype or B.dim() != 2 or B.device != device:
@@ -256,6 +269,8 @@ def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None
         C, ldc, c_type = B.new_empty((N, A.M)), A.M, _DTYPES[dtype]
     else:
         ldc, c_type = _output(C, (N, A.M), (dtype, torch.float32), device, "C"), _DTYPES[C.dtype]
+        if _overlap(B, ldb, C, ldc):
+            raise ValueError("C must not overlap B, which is read while C is written")
     ptr = B.data_ptr()
     need = lib.flashspmm_w4_matmul_workspace_bytes(A._ref, ptr, ldb, N)
     ws = _scratch(need, B)

@@ -172,6 +172,7 @@ def _rows(t: torch.Tensor) -> tuple:
 def _output(t, shape: tuple, dtypes, device: torch.device, name: str) -> int:
     """Checks an output that the caller gave; the distance of its rows."""
     _cuda(t, name, dtypes)
+    _no_grad(t)
     if t.shape != shape or t.device != device or (shape[1] > 1 and t.stride(1) != 1) or \
             (shape[0] > 1 and t.stride(0) < shape[1]):
         raise ValueError(f"{name} must be a {list(shape)} tensor on {device} with unit stride along its rows")

@@ -414,9 +414,12 @@ flashspmm_status flashspmm_w4_decode(const flashspmm_w4* A, void* W, int32_t w_d
  * current device; 0 when none. */
 size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B, int64_t ldb, int32_t N);
 
-/* Skinny product C = A x B with fp32 sums.  Up to N = 8 the sums are of s times
- * whole numbers q - z; above, a weight s * (q - z) may be rounded to A->dtype
- * first, as flashspmm_w4_decode gives it: the sizes decide, not where B lies.
+/* Skinny product C = A x B with fp32 sums.  With output in A->dtype and N > 8 a
+ * weight s * (q - z) may be rounded to A->dtype first, as flashspmm_w4_decode
+ * gives it (in fp16 one beyond 65504 is infinite then): the sizes decide, not
+ * where B lies.  Up to N = 8, and with FLASHSPMM_F32 output, no weight is rounded
+ * (fp32 output, N > 8: a weight beyond twice A->dtype's largest value may count as
+ * infinite).
  *   A          a view with count = 1.
  *   B          device, A->dtype, N rows of K activations, ldb values apart
  *              (any alignment; rows that start on 16 bytes with K % 8 == 0 are

@@ -138,3 +138,114 @@ def test_tensor_memory_kernel_in_graphs_and_streams(N, group):
         other = [fs.w4_matmul(A, b, stream=side) for b in Bs]
         torch.cuda.synchronize()
         assert torch.equal(out, want[i]) and all(torch.equal(a, b) for a, b in zip(other, want))
+
+
+# ---------------------------------------------------------------- fp32 output: no weight is rounded
+
+def launches(call):
+    before = fs.launch_count()
+    call()
+    return fs.launch_count() - before
+
+
+def check32(C, W, B):
+    """Sums over the weights and over their rests, 2 K / 16 steps of the tensor cores, and nothing else."""
+    want, size = B.double() @ W.t(), B.double().abs() @ W.abs().t()
+    bound = (2 * W.shape[1] / 16 + 64) * 2.0 ** -23 * size
+    off = (C.double() - want).abs()
+    assert (off <= bound).all(), f"{(off / bound).max().item():.3g} of the bound"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("N", [48, 64, 100, 128, 129, 256])
+def test_fp32_output(dtype, group, symmetric, N):
+    codes, scales, zeros = codes_of((M, K), group, dtype, symmetric, N)
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    B = torch.randn((N, K), device="cuda", generator=gen(N)).to(dtype)
+    C = torch.empty((N, M), device="cuda")
+    assert launches(lambda: fs.w4_matmul(A, B, C)) == 2  # rows on 16 bytes: one launch is fragments
+    check32(C, dense64(codes, scales, zeros, group), B)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("rows,columns,N", [(129, 65536, 40), (12288, 1032, 100), (40000, 136, 70), (128, 33001, 256),
+                                            (4099, 5003, 17), (1, 1, 256), (130, 120, 9), (8192, 8195, 24)])
+def test_fp32_output_shapes(rows, columns, N, group):
+    codes, scales, zeros = codes_of((rows, columns), group, torch.float16, False, N)
+    A = fs.w4_pack(codes, scales, zeros, group=group)
+    B = torch.randn((N, columns), device="cuda", generator=gen(N)).half()
+    C = torch.empty((N, rows), device="cuda")
+    check32(fs.w4_matmul(A, B, C), dense64(codes, scales, zeros, group), B)
+
+
+@pytest.mark.parametrize("N", [48, 140])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_fp32_output_over_the_range_of_scales(N, dtype):
+    """Rests of the smallest weights are whole steps of the type, and weights up to twice the largest value are exact."""
+    codes, _, zeros = codes_of((M, K), 64, dtype, False, 1)
+    fin = torch.finfo(dtype)
+    g = gen(3)
+    for low, high in ((fin.smallest_normal / 8, fin.smallest_normal * 4), (1e-3, 1e-2), (fin.max / 16, fin.max / 8)):
+        scales = (torch.rand((M, -(-K // 64)), device="cuda", generator=g).double() * (high - low) + low).to(dtype)
+        B = torch.randn((N, K), device="cuda", generator=g)
+        # sums of K weights of fin.max stay finite in bf16, and the smallest ones above fp32's own steps
+        B = (B * 2.0 ** -20 if high > 1 else B * 2.0 ** 20 if high < 1e-30 else B).to(dtype)
+        A = fs.w4_pack(codes, scales, zeros, group=64)
+        C = torch.empty((N, M), device="cuda")
+        check32(fs.w4_matmul(A, B, C), dense64(codes, scales, zeros, 64), B)
+
+
+@pytest.mark.parametrize("N", [48, 140])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_fp32_output_of_non_finite_activations(N, dtype):
+    codes, scales, zeros = codes_of((M, K), 32, dtype, True, 2)
+    codes[:, 5] = 9  # no weight of column 5 is zero; many of its rests are
+    A = fs.w4_pack(codes, scales, zeros, group=32)
+    B = torch.randn((N, K), device="cuda", generator=gen(1)).to(dtype)
+    want = fs.w4_matmul(A, B, torch.empty((N, M), device="cuda"))
+    for value in (float("inf"), -float("inf"), float("nan")):
+        for column in (5, 4):
+            B[N - 1, column] = value
+            got = fs.w4_matmul(A, B, torch.empty((N, M), device="cuda"))
+            assert torch.equal(got[:-1], want[:-1])
+            if column == 5:
+                assert torch.isnan(got[-1]).all() if value != value else (got[-1] == value).all()
+                B[N - 1, 5] = 1
+            else:  # weights of both signs and zero
+                w = dense64(codes, scales, zeros, 32)[:, 4]
+                assert torch.equal(torch.nan_to_num(got[-1].double(), nan=7, posinf=8, neginf=9),
+                                   torch.nan_to_num(w * value, nan=7, posinf=8, neginf=9))
+                B[N - 1, 4] = 1
+
+
+@pytest.mark.parametrize("N", [48, 140])
+def test_fp32_output_of_non_finite_scales(N):
+    codes, scales, zeros = codes_of((M, K), 64, torch.bfloat16, False, 2)
+    B = torch.randn((N, K), device="cuda", generator=gen(1)).bfloat16()
+    want = fs.w4_matmul(fs.w4_pack(codes, scales, zeros, group=64), B, torch.empty((N, M), device="cuda"))
+    scales[77, 3], scales[2590, 128] = float("inf"), float("nan")
+    got = fs.w4_matmul(fs.w4_pack(codes, scales, zeros, group=64), B, torch.empty((N, M), device="cuda"))
+    assert not torch.isfinite(got[:, [77, 2590]]).any()
+    got[:, [77, 2590]] = want[:, [77, 2590]]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("N", [48, 140])
+def test_fp32_output_strides_and_graphs(N):
+    codes, scales, zeros = codes_of((M, K), 128, torch.float16, False, 2)
+    A = fs.w4_pack(codes, scales, zeros)
+    B = torch.randn((N, K), device="cuda", generator=gen(1)).half()
+    want = fs.w4_matmul(A, B, torch.empty((N, M), device="cuda"))
+    wide = torch.full((N, K + 3), float("nan"), device="cuda", dtype=torch.float16)
+    wide[:, 1:1 + K] = B
+    out = torch.full((N, M + 9), 5.0, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fs.w4_matmul(A, wide[:, 1:1 + K], out[:, 4:4 + M])
+    for _ in range(3):
+        out[:, 4:4 + M] = 5
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:, 4:4 + M], want) and (out[:, :4] == 5).all() and (out[:, 4 + M:] == 5).all()

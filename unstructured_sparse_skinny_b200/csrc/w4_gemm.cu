@@ -19,6 +19,16 @@
 // them in their order.  Four warps do this behind the products; at the end of
 // its run the whole CTA joins in, since nothing is left to overlap with.
 //
+// The rounding of the weights is the price of an A operand of 16 bits that holds
+// the scale: half a step of the type a weight, independent of one another, which
+// with the output's own rounding makes an error 1.34 times that of the latter
+// alone (64 tokens of 12288^2, bf16: 2.2e-3 of the result's norm, 1.7e-3).
+//
+// For fp32 output the weights are not rounded: each unit is two steps, of the
+// weights rounded to 16 bits and of what that leaves, which 16 bits hold exactly.
+// The second step has its own image of the activations, zeros in place of what is
+// not finite: infinity times a rest of zero would be NaN.
+//
 // What bounds it: up to 128 tokens the warps that make the weights (12288^2, 64
 // tokens: 32 us; HBM would allow 12); at 256 tokens the
 // products, 1024 cycles a unit, and the clock under the power limit (9216 x 36864:
@@ -48,7 +58,7 @@ constexpr uint64_t kWaitBudgetNs = 1000000000ull;
 
 struct GemmParams {
   W4Dev A;
-  const uint8_t* image;  // [units][2][n_pad][128 bytes], swizzled
+  const uint8_t* image;  // [units, or steps of a block][2][n_pad][128 bytes], swizzled
   float* partials;       // [CTA][first, last block of its run][n_pad][128]
   int32_t* arrived;      // [blocks]
   void* C;
@@ -56,7 +66,7 @@ struct GemmParams {
   bool c_f32;
   int32_t N, n_pad;
   int32_t slots, ring;
-  int32_t steps;         // blocks * units
+  int32_t steps;         // blocks * units, twice that many for unrounded weights
   int* status;
 };
 
@@ -65,11 +75,13 @@ struct GemmParams {
 // One thread per row and 32-column block: position 16 s + 8 h + 2 t + e of a
 // block holds column 8 t + 4 s + 2 h + e.  A block is half a 128-byte row of
 // the tile, whose 16-byte chunks are exchanged by row (128-byte swizzle).
-template <bool Vec>
+// Split: two tiles a unit, the second without the values that are not finite;
+// `exponent` is the bits of an exponent in both halves of a word.
+template <bool Vec, bool Split>
 __global__ void __launch_bounds__(256) w4_stage_kernel(const uint16_t* __restrict__ B, int64_t ldb, int32_t N,
                                                        int32_t K, int32_t n_pad, int64_t blocks,
                                                        uint8_t* __restrict__ image, int32_t* __restrict__ arrived,
-                                                       int64_t row_blocks) {
+                                                       int64_t row_blocks, uint32_t exponent) {
   griddep_launch_dependents();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   for (int64_t j = i; j < row_blocks; j += static_cast<int64_t>(gridDim.x) * 256) arrived[j] = 0;
@@ -86,11 +98,23 @@ __global__ void __launch_bounds__(256) w4_stage_kernel(const uint16_t* __restric
     w[4 * t + 2] = v.z;
     w[4 * t + 3] = v.w;
   }
-  uint8_t* tile = image + (blk >> 1) * (static_cast<int64_t>(n_pad) * 128) + n * 128;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {  // c = 2 s + h
-    const int chunk = ((blk & 1) * 4 + c) ^ (n & 7);
-    *reinterpret_cast<uint4*>(tile + chunk * 16) = make_uint4(w[c], w[4 + c], w[8 + c], w[12 + c]);
+  for (int part = 0; part < (Split ? 2 : 1); ++part) {
+    const int64_t half = Split ? (blk >> 2) * 4 + part * 2 + (blk >> 1 & 1) : blk >> 1;
+    uint8_t* tile = image + half * (static_cast<int64_t>(n_pad) * 128) + n * 128;
+    if (part == 1) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t low = exponent & 0xFFFFu, high = exponent & 0xFFFF0000u;
+        if ((w[j] & low) == low) w[j] &= 0xFFFF0000u;
+        if ((w[j] & high) == high) w[j] &= 0xFFFFu;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {  // c = 2 s + h
+      const int chunk = ((blk & 1) * 4 + c) ^ (n & 7);
+      *reinterpret_cast<uint4*>(tile + chunk * 16) = make_uint4(w[c], w[4 + c], w[8 + c], w[12 + c]);
+    }
   }
 }
 
@@ -162,6 +186,40 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s, __nv_bfloat16) 
   return r;
 }
 
+// A weight has at most 8 + 6 (bf16) or 11 + 6 (fp16) significant bits, multiples of the type's smallest step: its
+// rounding's rest is exact in 16 bits too.  Up to twice the largest 16-bit value, that is: the rounding stops at the
+// largest, and a weight that both parts together cannot hold is infinite.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+  using Type = __half2;
+  static constexpr uint32_t kLargest = 0x7BFF7BFFu;
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  using Type = __nv_bfloat162;
+  static constexpr uint32_t kLargest = 0x7F7F7F7Fu;
+};
+template <typename T>
+__device__ __forceinline__ uint32_t part2(uint32_t a, uint32_t s, bool rest) {
+  union U {
+    uint32_t u;
+    typename Pair<T>::Type v;
+  } x, y, product, most, least;
+  x.u = a;
+  y.u = s;
+  product.u = mul2(a, s, T());
+  most.u = Pair<T>::kLargest;
+  least.u = Pair<T>::kLargest | 0x80008000u;
+  product.v = __hmax2_nan(__hmin2_nan(product.v, most.v), least.v);
+  if (rest) {
+    product.u ^= 0x80008000u;
+    product.v = __hfma2(x.v, y.v, product.v);
+  }
+  return product.u;
+}
+
 // The P-th part (128 / P columns) of one strip of it as a lane holds it: codes, then 16-bit weights.
 template <typename T, int NG, int P>
 struct Part {
@@ -212,7 +270,9 @@ struct Part {
     }
   }
 
-  __device__ __forceinline__ void weights(uint32_t (&r)[4 * kWords]) const {
+  // Split: in two parts, `rest` the second one.
+  template <bool Split>
+  __device__ __forceinline__ void weights(uint32_t (&r)[4 * kWords], bool rest) const {
 #pragma unroll
     for (int gi = 0; gi < kGroups; ++gi) {
       const W4Zero<T, 0> zero(static_cast<int>(z[gi] & 0xFF), static_cast<int>(z[gi] >> 8));
@@ -222,7 +282,8 @@ struct Part {
         uint32_t a[4];
         w4_fragment(w[i], zero, a);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[4 * i + j] = mul2(a[j], j & 1 ? s1 : s0, T());
+        for (int j = 0; j < 4; ++j)
+          r[4 * i + j] = Split ? part2<T>(a[j], j & 1 ? s1 : s0, rest) : mul2(a[j], j & 1 ? s1 : s0, T());
       }
     }
   }
@@ -396,7 +457,8 @@ __device__ __forceinline__ void join_block(const GemmParams& p, int32_t block, c
 }
 
 // P (1 or 4): warps share the columns of 32 rows of a unit P ways, so 4 / P groups of 4 P warps have units in turn.
-template <typename T, int NG, int P>
+// Split: two steps a unit, see part2.
+template <typename T, int NG, int P, bool Split>
 __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t codes_full[kMaxRing], codes_used[kMaxRing], full[kMaxSlots], used[kMaxSlots], acc_full[2], acc_empty[2], mma_done[2];
@@ -404,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
   __shared__ int abort_word, last_word;
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t units = p.A.units;
+  constexpr int kSteps = Split ? 2 : 1;  // of a unit
+  const int32_t units = p.A.units * kSteps;
   const Runs runs(p.steps, gridDim.x);
   const int32_t q0 = runs.begin(blockIdx.x), q1 = runs.begin(blockIdx.x + 1);
   const uint32_t stage_bytes = static_cast<uint32_t>(p.n_pad) * 256, unit_bytes = 8 * p.A.record;
@@ -462,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
       for (int j = 0; j < 2; ++j) {
         Part<T, NG, P> strip;
         strip.load(record + j * p.A.record, part, lane, zeros);
-        strip.weights(r[j % kHeld]);
+        strip.template weights<Split>(r[j % kHeld], q & 1);
         if (j == kHeld - 1) {
           ready = mbar_wait(&used[slot], phase, abort_flag, kWaitBudgetNs, p.status);
           if (!ready) break;
@@ -584,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
     const uint32_t bytes = of_codes ? unit_bytes : stage_bytes;
     // a block's units are consecutive: step q is the matrix's q-th
     int32_t u = q0 % units;
-    const uint8_t* from = of_codes ? p.A.data + static_cast<int64_t>(q0) * unit_bytes
+    const uint8_t* from = of_codes ? p.A.data + static_cast<int64_t>(q0 / kSteps) * unit_bytes
                                    : p.image + static_cast<int64_t>(u) * stage_bytes;
     uint8_t* to = of_codes ? codes : tiles;
     int32_t left = q1 - q0;
@@ -597,8 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_gemm_kernel(const GemmParams p
         bulk_load(to + slot * bytes, from, bytes, &filled[slot]);
       }
       __syncwarp();
-      from += bytes;
-      if (++u == units) {
+      ++u;
+      if (!Split || !of_codes || (u & 1) == 0) from += bytes;
+      if (u == units) {
         u = 0;
         if (!of_codes) from = p.image;
       }
@@ -662,13 +726,13 @@ GemmWorkspace layout(int32_t M, int32_t K, int32_t N) {
   const int32_t units = w4_units(K);
   GemmWorkspace w;
   w.image = 0;
-  w.partials = static_cast<size_t>(units) * pad_n(N) * 256;
+  w.partials = static_cast<size_t>(units) * pad_n(N) * 256 * 2;  // fp32 output needs both tiles of a unit
   w.arrived = w.partials + static_cast<size_t>(ctas_of(blocks, units)) * 2 * pad_n(N) * kBlockRows * sizeof(float);
   w.bytes = w.arrived + (static_cast<size_t>(blocks) * sizeof(int32_t) + 15) / 16 * 16;
   return w;
 }
 
-template <typename T, int NG, int P>
+template <typename T, int NG, int P, bool Split>
 cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
   // P = 1: four groups of warps have units in turn, each a slot of its own.  P = 4, for tiles of which only three
   // fit: all warps on each unit.  (Two groups of two ways with two slots each: 34 instead of 32 us for 64 tokens of
@@ -676,7 +740,7 @@ cudaError_t launch_as(GemmParams& p, int64_t ctas, cudaStream_t s) {
   p.slots = P == 1 ? 4 : 3;
   p.ring = static_cast<int32_t>(min64(kMaxRing, (kSharedBytes - p.slots * p.n_pad * 256) / (8 * p.A.record))) / 4 *
            4 * (P == 1) + 3 * (P == 4);
-  auto kernel = w4_gemm_kernel<T, NG, P>;
+  auto kernel = w4_gemm_kernel<T, NG, P, Split>;
   static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -720,22 +784,28 @@ cudaError_t launch_w4_gemm(const flashspmm_w4* in, const void* B, int64_t ldb, v
   p.status = device_status_ptr();
   if (!p.status) return cudaErrorInitializationError;
   const int64_t blocks = (static_cast<int64_t>(p.A.M) + kBlockRows - 1) / kBlockRows;
-  if (blocks * p.A.units > INT32_MAX) return cudaErrorInvalidValue;  // 16 TB of codes
-  p.steps = static_cast<int32_t>(blocks * p.A.units);
+  const int64_t steps = blocks * p.A.units * (c_f32 ? 2 : 1);
+  if (steps > INT32_MAX) return cudaErrorInvalidValue;  // 8 TB of codes
+  p.steps = static_cast<int32_t>(steps);
 
   const int64_t k_blocks = static_cast<int64_t>(p.A.units) * 4;
   const dim3 grid(static_cast<unsigned>((k_blocks * p.n_pad + 255) / 256));
   const uint16_t* b = static_cast<const uint16_t*>(B);
+  const uint32_t exponent = in->dtype == FLASHSPMM_F16 ? 0x7C007C00u : 0x7F807F80u;
+#define FLASHSPMM_STAGE(VEC, SPLIT) \
+  w4_stage_kernel<VEC, SPLIT><<<grid, 256, 0, s>>>(b, ldb, N, p.A.K, p.n_pad, k_blocks, base + w.image, p.arrived, blocks, exponent)
   if (rows_aligned(B, ldb, p.A.K))
-    w4_stage_kernel<true><<<grid, 256, 0, s>>>(b, ldb, N, p.A.K, p.n_pad, k_blocks, base + w.image, p.arrived, blocks);
+    c_f32 ? FLASHSPMM_STAGE(true, true) : FLASHSPMM_STAGE(true, false);
   else
-    w4_stage_kernel<false><<<grid, 256, 0, s>>>(b, ldb, N, p.A.K, p.n_pad, k_blocks, base + w.image, p.arrived, blocks);
+    c_f32 ? FLASHSPMM_STAGE(false, true) : FLASHSPMM_STAGE(false, false);
+#undef FLASHSPMM_STAGE
   note_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
   const int64_t ctas = ctas_of(blocks, p.A.units);
-#define FLASHSPMM_BY_PARTS(T, NG) (p.n_pad <= 128 ? launch_as<T, NG, 1>(p, ctas, s) : launch_as<T, NG, 4>(p, ctas, s))
+#define FLASHSPMM_BY_OUTPUT(T, NG, P) (c_f32 ? launch_as<T, NG, P, true>(p, ctas, s) : launch_as<T, NG, P, false>(p, ctas, s))
+#define FLASHSPMM_BY_PARTS(T, NG) (p.n_pad <= 128 ? FLASHSPMM_BY_OUTPUT(T, NG, 1) : FLASHSPMM_BY_OUTPUT(T, NG, 4))
 #define FLASHSPMM_BY_GROUP(T)                          \
   e = p.A.group == 128  ? FLASHSPMM_BY_PARTS(T, 1)     \
       : p.A.group == 64 ? FLASHSPMM_BY_PARTS(T, 2)     \
@@ -746,6 +816,7 @@ cudaError_t launch_w4_gemm(const flashspmm_w4* in, const void* B, int64_t ldb, v
     FLASHSPMM_BY_GROUP(__nv_bfloat16);
 #undef FLASHSPMM_BY_GROUP
 #undef FLASHSPMM_BY_PARTS
+#undef FLASHSPMM_BY_OUTPUT
   note_launch();
   return e;
 }

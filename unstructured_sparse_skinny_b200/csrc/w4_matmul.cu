@@ -104,21 +104,25 @@ cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K
 // there 8.5 (two kernels, the joining of blocks) and 0.27 per 1000 records.  The
 // two round differently, so the choice goes by the sizes alone and not by where
 // the activations lie (those that have to be copied first cost 2.5 us more here).
-static bool by_fragments(const flashspmm_w4* A, int32_t N) {
+// For fp32 output, whose records are two steps there, 0.7 (64 tokens of 12288^2
+// take 77 us, 16-bit output 38; on fragments 16 tokens take 53).
+static bool by_fragments(const flashspmm_w4* A, int32_t N, bool c_f32) {
   if (N <= 8) return true;
   const double records = 8e-3 * w4_blocks(A->M) * w4_units(A->K);
   const double each = A->group == 32 ? 0.3 : 0.24;
-  return 3.5 + each * ((N + 7) / 8) * records < 8.5 + 0.27 * records;
+  return 3.5 + each * ((N + 7) / 8) * records < 8.5 + (c_f32 ? 0.7 : 0.27) * records;
 }
 
+// Enough for either output: fp32 goes by fragments whenever 16 bits do, and the image that tcgen05 takes is larger
+// than a copy of the activations.
 size_t w4_matmul_workspace(const flashspmm_w4* A, int32_t N, bool aligned) {
-  if (!by_fragments(A, N)) return w4_gemm_workspace(A->M, A->K, N);
+  if (!by_fragments(A, N, false)) return w4_gemm_workspace(A->M, A->K, N);
   return aligned ? 0 : static_cast<size_t>(N) * aligned_k(A->K) * 2;
 }
 
 cudaError_t launch_w4_matmul(const flashspmm_w4* in, const void* B, int64_t ldb, void* C, int64_t ldc, bool c_f32,
                              int32_t N, void* workspace, cudaStream_t s) {
-  if (!by_fragments(in, N)) return launch_w4_gemm(in, B, ldb, C, ldc, c_f32, N, workspace, s);
+  if (!by_fragments(in, N, c_f32)) return launch_w4_gemm(in, B, ldb, C, ldc, c_f32, N, workspace, s);
   MatmulParams p{};
   p.A = w4_dev(in);
   if (!rows_aligned(B, ldb, p.A.K)) {

@@ -253,7 +253,9 @@ def w4_decode(A: W4, dtype: torch.dtype | None = None, stream=None) -> torch.Ten
 def w4_matmul(A: W4, B: torch.Tensor, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """C = A x B for a skinny B.  B is ``[N, K]`` in A's type with N = 1..256
     (rows may be apart); returns C as ``[N, M]`` in that type, or writes the
-    given C, which may be float32 (the unrounded sums) and must not overlap B."""
+    given C, which must not overlap B.  With a 16-bit C and N > 8 weights may be
+    rounded to that type before the product; with a float32 C neither weights
+    nor sums are (about twice the time for large N)."""
     lib = binding._lib or binding.load_library()
     device, dtype = A.data.device, A.dtype
     if B.dtype is not dtype or B.dim() != 2 or B.device != device:

@@ -99,13 +99,14 @@ cudaError_t launch_align_rows(const void* X, int64_t ld, int32_t rows, int32_t K
   return cudaGetLastError();
 }
 
-// Eight tokens at a time here, or all at once by tcgen05?  Measured, in us: here
+// Eight tokens at a time here, or all at once by tcgen05?  Fitted, in us: here
 // 3.5 and 0.24 per 1000 records for every eight tokens, 0.3 with groups of 32;
-// there 8.5 (two kernels, the joining of blocks) and 0.27 per 1000 records.  The
-// two round differently, so the choice goes by the sizes alone and not by where
-// the activations lie (those that have to be copied first cost 2.5 us more here).
-// For fp32 output, whose records are two steps there, 0.7 (64 tokens of 12288^2
-// take 77 us, 16-bit output 38; on fragments 16 tokens take 53).
+// there 8.5 (two kernels, the joining of blocks) and 0.27 per 1000 records, for
+// fp32 output, whose records are two steps there, 0.7.  The two round differently,
+// so the choice goes by the sizes alone and not by where the activations lie
+// (those that have to be copied first cost 2.5 us more here).  Measured, here and
+// there, codes from HBM: 4096^2, 24 tokens 16 and 17, 32 tokens 21 and 19; 12288^2,
+// 16 tokens 53 and 34; fp32 output of 8192^2, 24 tokens 41 and 42, 32 tokens 47 and 42.
 static bool by_fragments(const flashspmm_w4* A, int32_t N, bool c_f32) {
   if (N <= 8) return true;
   const double records = 8e-3 * w4_blocks(A->M) * w4_units(A->K);

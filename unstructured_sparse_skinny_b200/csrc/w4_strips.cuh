@@ -127,9 +127,6 @@ struct StripAt {
 __device__ __forceinline__ void copy_or_zero(uint32_t to, const void* from, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(copy ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
 
 // The shared memory a warp's units arrive in: places of a pair of records.
 template <int NG>
@@ -141,20 +138,19 @@ struct StripRing {
     const uint32_t to = smem_u32(base) + place * kPlace;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      copy16(to + r * kRecord + lane * 16, from[r] + lane * 16);
-      copy16(to + r * kRecord + 512 + lane * 16, from[r] + 512 + lane * 16);
+      cp_async_16(to + r * kRecord + lane * 16, from[r] + lane * 16);
+      cp_async_16(to + r * kRecord + 512 + lane * 16, from[r] + 512 + lane * 16);
     }
     // scales and zero points: half a warp a record
     const int piece = lane & 15;
     const bool second = lane >= 16;
     if (piece < ((second ? zeros[1] : zeros[0]) ? 3 * NG : 2 * NG))
-      copy16(to + (second ? kRecord : 0) + kW4CodeBytes + piece * 16,
+      cp_async_16(to + (second ? kRecord : 0) + kW4CodeBytes + piece * 16,
              (second ? from[1] : from[0]) + kW4CodeBytes + piece * 16);
   }
-  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // The oldest of kStripRing groups has arrived, for the whole warp.
   static __device__ __forceinline__ void wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStripRing - 1) : "memory");
+    cp_async_wait<kStripRing - 1>();
     __syncwarp();
   }
 };
@@ -177,7 +173,7 @@ __device__ __forceinline__ void strip_product(const StripAt (&at)[2], int32_t un
   const bool zeros[2] = {at[0].zeros, at[1].zeros};
   const auto ask = [&](int place) {
     if (asked < units) ring.ask(place, from, zeros, lane);
-    ring.commit();
+    cp_async_commit();
     asked += ways;
 #pragma unroll
     for (int r = 0; r < 2; ++r) from[r] += static_cast<int64_t>(ways) * at[r].pitch;
@@ -258,10 +254,15 @@ __device__ __forceinline__ void strip_reduce(const float (&acc)[2][NT][4], int p
 }
 
 // Host: pairs of strips a CTA takes, for `sets` sets of `pairs` with `rows`
-// activation rows each.  The CTAs run in waves of two on each SM; a CTA's time
-// is its records', the staging of the activations and a fixed part, in records
-// (22 KB/us for each of 296 CTAs at the rate of HBM: a record is 0.05 us, the
-// fixed part some 3 us; staging a row's unit is a tenth of a record).
+// activation rows each.  The CTAs run in waves of `resident` on each SM; a CTA's
+// time is its records', the staging of the activations and a fixed part, in
+// records, as fitted with two CTAs an SM (22 KB/us for each of 296 at the rate of
+// HBM: a record is 0.05 us, the fixed part some 3 us; staging a row's unit is a
+// tenth of a record).  With one and three an SM the constants are the same: the
+// choice is within 3 % of the best of 1, 2, 4 and 8 in all (us by this rule, and
+// by each: 4 tokens, 8 experts of 4096 x 11008, 120, 134 124 121 120; 8 tokens, 64
+// of 4096 x 2048, 217, 235 214 212 216; 64 tokens, 288, 482 360 302 289; 64 tokens,
+// 4 of 4096 x 4096, 243, 431 325 261 302).
 inline int32_t pairs_per_cta(double sets, int32_t pairs, int32_t units, double rows, int resident) {
   const int sms = device_sm_count();
   const double wave = static_cast<double>(resident) * (sms > 0 ? sms : 1);

@@ -30,9 +30,10 @@
 // not finite: infinity times a rest of zero would be NaN.
 //
 // What bounds it: up to 128 tokens the warps that make the weights (12288^2, 64
-// tokens: 32 us; HBM would allow 12); at 256 tokens the
+// tokens: 35 us; HBM would allow 12); at 256 tokens the
 // products, 1024 cycles a unit, and the clock under the power limit (9216 x 36864:
-// 135 to 148 us, 1.2 to 1.3 PFLOP/s).  Some 8 us a call are fixed: two kernels, the
+// 128 us, 1.36 PFLOP/s, alone at 1965 MHz; 172 us, 1.01 PFLOP/s, in a loop at the
+// 1305 MHz that 1000 W leave).  Some 8 us a call are fixed: two kernels, the
 // ends of the runs and the joining of shared blocks.
 #include <atomic>
 #include <type_traits>

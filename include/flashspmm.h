@@ -391,10 +391,10 @@ int64_t flashspmm_w4_bytes(int32_t M, int32_t K, int32_t count, int32_t group, i
  *   symmetric  1: s = max|w| / 7, z = 8 (A->zeros must be 0).
  *              0: s = (max(w, 0) - min(w, 0)) / 15, z = round(-min(w, 0) / s)
  *              clamped to 0..15 (A->zeros must be 1).
- * s is rounded to A->dtype and q = clamp(round(w / s) + z, 0, 15); roundings
- * are to nearest, ties to even.  A group whose s is zero has q = z.  A group
- * with a NaN or an infinity gets such a scale, so it decodes to values that
- * are not finite. */
+ * The difference and the first quotient are fp32, s is rounded to A->dtype and
+ * q = clamp(round(w / s) + z, 0, 15); roundings are to nearest, ties to even.  A
+ * group whose s is zero has q = z.  A group with a NaN or an infinity gets such a
+ * scale, so it decodes to values that are not finite. */
 flashspmm_status flashspmm_w4_encode(const void* W, int64_t ldw, int32_t symmetric, const flashspmm_w4* A,
                                      void* stream);
 
@@ -432,7 +432,8 @@ size_t flashspmm_w4_matmul_workspace_bytes(const flashspmm_w4* A, const void* B,
  *              needs no initialisation.  Calls that may run concurrently need
  *              separate ones.
  * Results are deterministic.  K == 0 writes zeros; M == 0 or N == 0 does
- * nothing. */
+ * nothing.  Waits inside the kernels are bounded as in the SpMM: one that runs
+ * out leaves wrong values and an error for flashspmm_get_device_status. */
 flashspmm_status flashspmm_w4_matmul(const flashspmm_w4* A, const void* B, int64_t ldb, void* C, int64_t ldc,
                                      int32_t c_dtype, int32_t N, void* workspace, size_t workspace_bytes,
                                      void* stream);
@@ -457,7 +458,8 @@ size_t flashspmm_moe_w4_workspace_bytes(const flashspmm_w4* gate, const void* X,
  *   router     device, E x H row-major, dtype or FLASHSPMM_F32 (router_dtype).
  *              Logits are summed in some 46 bits; two that are closer than that
  *              may come out in either order, equal rows of the router are a tie.
- *              A NaN logit is chosen last and its token's p are NaN.
+ *              Products and sums beyond fp32's range are infinite.  A NaN logit
+ *              is chosen last and its token's p are NaN.
  *              NULL: ids and weights are inputs, a routing of the caller's.
  *              An id outside 0 .. E - 1 contributes nothing, one named twice
  *              by a token counts with the sum of its weights.

@@ -11,8 +11,9 @@ Every call runs on the device of its tensors.  ``stream`` is a
 device; outputs and scratch are allocated on the stream the call runs on, so
 calls on different streams share nothing and every call can be captured in a
 CUDA graph.  Inputs made on another stream are ordered by the caller, as with
-torch's own operators.  These are inference calls: an input that requires
-grad is refused while grad mode is on.
+torch's own operators.  Errors that a kernel finds are read with
+``check_device_status``.  These are inference calls: an input, or an output
+that the caller gives, that requires grad is refused while grad mode is on.
 """
 from __future__ import annotations
 

@@ -118,9 +118,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
 // sum is multiplied by w4_raise.  At the other end sums are kept to 2^-136
 // instead of 2^-149.  (fp16 activations are below 2^16.)
 template <typename T>
-constexpr int kW4Down = 0;  // binary orders
+inline constexpr int kW4Down = 0;  // binary orders
 template <>
-constexpr int kW4Down<__nv_bfloat16> = 13;
+inline constexpr int kW4Down<__nv_bfloat16> = 13;
 template <typename T>
 __device__ __forceinline__ float w4_raise(float sum) {
   return kW4Down<T> ? sum * static_cast<float>(1 << kW4Down<T>) : sum;
